@@ -10,6 +10,9 @@ LIB_PATH = os.environ.get("LIBMOE_PATH", os.path.join(PKG, "libmoe.so"))
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
 
+SCORES = {"softmax": 0, "sigmoid": 1}         # libmoe_route.h: moe_score
+GROUP_RANKS = {"max": 0, "top2": 1}           # moe_group_rank
+
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_HIP"}
 
@@ -19,6 +22,10 @@ EXPORTS = ("moe_router", "moe_gate", "moe_gate_record", "moe_stage_to_host", "mo
            "moe_grouped_ffn_packed", "moe_grouped_ffn_fp8w",
            "moe_grouped_ffn_fp8w_packed", "moe_combine",
            "moe_stats", "moe_prob_signature", "moe_status_string")
+
+# the symbols of include/libmoe_route.h and include/libmoe_int8.h
+ROUTE_EXPORTS = ("moe_route",)
+INT8_EXPORTS = ("moe_quantize_rows_i8", "moe_grouped_linear_i8", "moe_grouped_ffn_i8")
 
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -44,6 +51,11 @@ SIGNATURES = {
                              _sz, _p],
     "moe_grouped_ffn_fp8w_packed": [_p, _p, _i32, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _p, _p,
                              _sz, _p],
+    "moe_route": [_p, _i32, _p, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _p, _p, _p],
+    "moe_quantize_rows_i8": [_p, _i32, _i32, _i32, _p, _p, _p],
+    "moe_grouped_linear_i8": [_p, _p, _p, _i32, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _p],
+    "moe_grouped_ffn_i8": [_p, _p, _i32, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _p, _p,
+                           _sz, _p],
 }
 
 

@@ -51,6 +51,12 @@ def _out(t: torch.Tensor, name: str, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _same_device(first: torch.Tensor, **others: Optional[torch.Tensor]):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
 def _workspace(fn, args_before_ws, dev) -> torch.Tensor:
     """Query a call's workspace size (NULL workspace) and allocate it."""
     n = ctypes.c_size_t(0)
@@ -117,6 +123,38 @@ def gate_record(logits: torch.Tensor, k: int, block_tokens: int, layer: int, blo
     check("moe_gate_record", lib.moe_gate_record(_ptr(logits), T, E, k, int(bool(renormalize)), _ptr(topk_ids),
                                                  _ptr(topk_w), block_tokens, layer, L, _ptr(block_counts),
                                                  _stream(dev)))
+    return topk_ids, topk_w
+
+
+def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+          n_groups: int = 1, top_groups: Optional[int] = None, group_rank: str = "max", renormalize: bool = True,
+          scale: float = 1.0, topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None):
+    """k experts and weights per token from scores (moe_route): softmax or
+    sigmoid of the logits [T][E] (fp32 or bf16), `bias` ([E] fp32) added for the
+    selection only, the experts in `n_groups` groups of which the `top_groups`
+    best stay (all, if not given), weights renormalised and scaled."""
+    _need(logits, "logits", None, 2)
+    T, E = logits.shape
+    dev = logits.device
+    if score not in _lib.SCORES:
+        raise ValueError(f"score must be one of {sorted(_lib.SCORES)}")
+    if group_rank not in _lib.GROUP_RANKS:
+        raise ValueError(f"group_rank must be one of {sorted(_lib.GROUP_RANKS)}")
+    if bias is not None:
+        _out(bias, "bias", torch.float32, (E,))
+    if topk_ids is None:
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _out(topk_ids, "topk_ids", torch.int32, (T, k))
+    _out(topk_w, "topk_w", torch.float32, (T, k))
+    _same_device(logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
+    lib = _lib.load()
+    with torch.cuda.device(dev):
+        check("moe_route", lib.moe_route(
+            _ptr(logits), _dtype_code(logits), _ptr(bias), T, E, k, _lib.SCORES[score], n_groups,
+            n_groups if top_groups is None else top_groups, _lib.GROUP_RANKS[group_rank], int(bool(renormalize)),
+            float(scale), _ptr(topk_ids), _ptr(topk_w), _stream(dev)))
     return topk_ids, topk_w
 
 
@@ -474,6 +512,123 @@ def grouped_ffn_fp8w(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_sha
         _ptr(x), _ptr(x_rows), x.shape[0] if x_rows is not None else 0, _ptr(group_offsets), n_rows, E, n_shared,
         nseg, d, I, _ptr(w_gate), _ptr(s_gate), _ptr(w_up), _ptr(s_up), _ptr(w_down), _ptr(s_down), _ptr(h_sorted),
         _ptr(workspace), ctypes.byref(nbytes), _stream(dev)))
+    return h_sorted
+
+
+def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None):
+    """int8 codes [..][d] and fp32 scales [..] of the rows of x [..][d] (bf16 or
+    fp32): scale = max|row| / 127, codes to the nearest, halves to even
+    (moe_quantize_rows_i8).  Serves token rows and, once, weights."""
+    _need(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dim")
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    if s is None:
+        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _out(q, "q", torch.int8, x.shape)
+    _out(s, "s", torch.float32, x.shape[:-1])
+    _same_device(x, q=q, s=s)
+    lib = _lib.load()
+    with torch.cuda.device(x.device):
+        check("moe_quantize_rows_i8", lib.moe_quantize_rows_i8(_ptr(x), _dtype_code(x), s.numel(), x.shape[-1],
+                                                               _ptr(q), _ptr(s), _stream(x.device)))
+    return q, s
+
+
+def pack_i8_codes(q: torch.Tensor) -> torch.Tensor:
+    """int8 matrices [..][R][K] in the layout the int8 products read (blocks of
+    16 rows x 64 codes, the layout of pack_fp8_codes); same shape."""
+    if q.dtype != torch.int8:
+        raise TypeError(f"q must be {torch.int8}, got {q.dtype}")
+    return pack_fp8_codes(q)
+
+
+def _i8_batch(x_rows, group_offsets, E, n_shared, nseg, n_x):
+    """Checks of a grouped int8 call's row list and offsets; its sorted rows."""
+    _need(group_offsets, "group_offsets", torch.int32, 1)
+    if group_offsets.numel() != nseg * E + n_shared + 1:
+        raise ValueError("group_offsets must have nseg*E + n_shared + 1 entries")
+    if x_rows is None:
+        return n_x
+    _need(x_rows, "x_rows", torch.int32, 1)
+    return x_rows.numel()
+
+
+def grouped_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, group_offsets: torch.Tensor, E: int, n_shared: int,
+                      nseg: int, w: torch.Tensor, w_scale: torch.Tensor, y: Optional[torch.Tensor] = None,
+                      x_rows: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y[n] = x_scale * w_scale * (xq . w[expert of row n]) with int8 rows
+    [n_x][K] and packed int8 matrices [E+S][O][K] (pack_i8_codes); bf16 or fp32
+    out (y's dtype, or `out_dtype`).  E = 1 with offsets [0, N] is a plain
+    linear map (moe_grouped_linear_i8)."""
+    _need(xq, "xq", torch.int8, 2)
+    n_x, K = xq.shape
+    _out(x_scale, "x_scale", torch.float32, (n_x,))
+    _need(w, "w", torch.int8, 3)
+    N = _i8_batch(x_rows, group_offsets, E, n_shared, nseg, n_x)
+    O = w.shape[1]
+    if w.shape != (E + n_shared, O, K):
+        raise ValueError("w must be [E+S][O][K]")
+    _out(w_scale, "w_scale", torch.float32, (E + n_shared, O))
+    if y is None:
+        y = torch.empty((N, O), dtype=out_dtype, device=xq.device)
+    _out(y, "y", y.dtype, (N, O))
+    _same_device(xq, x_scale=x_scale, group_offsets=group_offsets, w=w, w_scale=w_scale, y=y, x_rows=x_rows)
+    lib = _lib.load()
+    with torch.cuda.device(xq.device):
+        check("moe_grouped_linear_i8", lib.moe_grouped_linear_i8(
+            _ptr(xq), _ptr(x_scale), _ptr(x_rows), n_x, _ptr(group_offsets), N, E, n_shared, nseg, K, O, _ptr(w),
+            _ptr(w_scale), _dtype_code(y), _ptr(y), _stream(xq.device)))
+    return y
+
+
+def ffn_i8_workspace_bytes(n_rows, n_x, d, I, E=1, n_shared=0, nseg=1) -> int:
+    """Workspace of grouped_ffn_i8: the int8 token rows (n_x of them; n_rows
+    without a row list), the int8 SwiGLU product, and their scales."""
+    lib = _lib.load()
+    n = ctypes.c_size_t(0)
+    check("moe_grouped_ffn_i8", lib.moe_grouped_ffn_i8(None, None, n_x, None, n_rows, E, n_shared, nseg, d, I, None,
+                                                       None, None, None, None, None, None, None, ctypes.byref(n),
+                                                       None))
+    return int(n.value)
+
+
+def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_shared: int, nseg: int,
+                   w_gate: torch.Tensor, s_gate: torch.Tensor, w_up: torch.Tensor, s_up: torch.Tensor,
+                   w_down: torch.Tensor, s_down: torch.Tensor, h_sorted: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, x_rows: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The expert FFN with packed int8 weights (pack_i8_codes), fp32 channel
+    scales and int8 activations; bf16 token rows, read directly or through
+    `x_rows`, bf16 out (moe_grouped_ffn_i8)."""
+    _need(x, "x", torch.bfloat16, 2)
+    for t, n in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
+        _need(t, n, torch.int8, 3)
+    n_x, d = x.shape
+    N = _i8_batch(x_rows, group_offsets, E, n_shared, nseg, n_x)
+    I = w_gate.shape[1]
+    G = E + n_shared
+    if w_gate.shape != (G, I, d) or w_up.shape != w_gate.shape or w_down.shape != (G, d, I):
+        raise ValueError("expert weight codes must be [E+S][I][d] (gate, up) and [E+S][d][I] (down)")
+    for t, n, width in ((s_gate, "s_gate", I), (s_up, "s_up", I), (s_down, "s_down", d)):
+        _out(t, n, torch.float32, (G, width))
+    dev = x.device
+    if h_sorted is None:
+        h_sorted = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+    _out(h_sorted, "h_sorted", torch.bfloat16, (N, d))
+    if workspace is None:
+        workspace = torch.empty(max(ffn_i8_workspace_bytes(N, n_x, d, I, E, n_shared, nseg), 256), dtype=torch.uint8,
+                                device=dev)
+    _need(workspace, "workspace", torch.uint8, 1)
+    _same_device(x, group_offsets=group_offsets, w_gate=w_gate, s_gate=s_gate, w_up=w_up, s_up=s_up, w_down=w_down,
+                 s_down=s_down, h_sorted=h_sorted, workspace=workspace, x_rows=x_rows)
+    lib = _lib.load()
+    nbytes = ctypes.c_size_t(workspace.numel())
+    with torch.cuda.device(dev):
+        check("moe_grouped_ffn_i8", lib.moe_grouped_ffn_i8(
+            _ptr(x), _ptr(x_rows), n_x, _ptr(group_offsets), N, E, n_shared, nseg, d, I, _ptr(w_gate), _ptr(s_gate),
+            _ptr(w_up), _ptr(s_up), _ptr(w_down), _ptr(s_down), _ptr(h_sorted), _ptr(workspace), ctypes.byref(nbytes),
+            _stream(dev)))
     return h_sorted
 
 

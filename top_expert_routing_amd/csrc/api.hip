@@ -6,6 +6,8 @@
 #include <mutex>
 
 #include "libmoe.h"
+#include "libmoe_int8.h"
+#include "libmoe_route.h"
 #include "launch.h"
 
 namespace {
@@ -157,9 +159,118 @@ moe_status ffn_call(const void* x_sorted, const int32_t* x_rows, int32_t n_x, co
   return hip_status(moe::launch_ffn(a, workspace, stream));
 }
 
+// Checks shared by the grouped int8 calls: the batch (before any workspace
+// query) and its row list and offsets.
+moe_status grouped_i8_sizes(int32_t n_rows, int32_t E, int32_t n_shared, int32_t nseg, int32_t K, int32_t O) {
+  if (n_rows < 0 || E < 1 || n_shared < 0 || (nseg != 1 && nseg != 2) || K < 1 || O < 1) return MOE_ERR_INVALID_ARG;
+  if (E > MOE_MAX_EXPERTS || n_shared > MOE_MAX_SHARED) return MOE_ERR_UNSUPPORTED;
+  if (K % 64 != 0 || O % 64 != 0 || K > 131072) return MOE_ERR_UNSUPPORTED;
+  if (!fits_int(static_cast<long long>(n_rows) * K) || !fits_int(static_cast<long long>(n_rows) * O) ||
+      !fits_int(static_cast<long long>(K) * O))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+moe_status moe_route(const void* logits, moe_dtype dtype, const float* bias, int32_t T, int32_t E, int32_t k,
+                     moe_score score, int32_t n_groups, int32_t top_groups, moe_group_rank group_rank,
+                     int32_t renormalize, float scale, int32_t* topk_ids, float* topk_w, hipStream_t stream) {
+  if (T < 0 || E < 1 || k < 1 || n_groups < 1 || E % n_groups != 0 || top_groups < 1 || top_groups > n_groups)
+    return MOE_ERR_INVALID_ARG;
+  if (static_cast<long long>(k) > static_cast<long long>(top_groups) * (E / n_groups)) return MOE_ERR_INVALID_ARG;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (group_rank != MOE_RANK_MAX && group_rank != MOE_RANK_TOP2) return MOE_ERR_INVALID_ARG;
+  if ((renormalize != 0 && renormalize != 1) || !__builtin_isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (!known_dtype(dtype) || E > MOE_MAX_EXPERTS || n_groups > MOE_MAX_EXPERT_GROUPS) return MOE_ERR_UNSUPPORTED;
+  if (!fits_int(static_cast<long long>(T) * E)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  const uintptr_t la = reinterpret_cast<uintptr_t>(logits);
+  if ((la & (elem_bytes(dtype) - 1)) != 0 || !aligned4(topk_ids) || !aligned4(topk_w) || (bias && !aligned4(bias)))
+    return MOE_ERR_INVALID_ARG;
+  moe::RouteArgs a;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.bf16 = dtype == MOE_BF16 ? 1 : 0;
+  a.sigmoid = score == MOE_SCORE_SIGMOID ? 1 : 0;
+  a.n_groups = n_groups;
+  a.top_groups = top_groups;
+  a.top2 = group_rank == MOE_RANK_TOP2 ? 1 : 0;
+  a.renormalize = renormalize;
+  a.scale = scale;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  return hip_status(moe::launch_route(logits, bias, a, stream));
+}
+
+moe_status moe_quantize_rows_i8(const void* x, moe_dtype dtype, int32_t T, int32_t d, int8_t* q, float* s,
+                                hipStream_t stream) {
+  if (T < 0 || d < 1) return MOE_ERR_INVALID_ARG;
+  if (!known_dtype(dtype) || d % 8 != 0 || !fits_int(static_cast<long long>(T) * d)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !s) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned4(s) || (reinterpret_cast<uintptr_t>(q) & 7u) != 0) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_quantize_rows(x, dtype == MOE_BF16 ? 1 : 0, T, d, q, s, stream));
+}
+
+moe_status moe_grouped_linear_i8(const int8_t* xq, const float* x_scale, const int32_t* x_rows, int32_t n_x,
+                                 const int32_t* group_offsets, int32_t n_rows, int32_t E, int32_t n_shared,
+                                 int32_t nseg, int32_t K, int32_t O, const int8_t* w, const float* w_scale,
+                                 moe_dtype out_dtype, void* y, hipStream_t stream) {
+  const moe_status st = grouped_i8_sizes(n_rows, E, n_shared, nseg, K, O);
+  if (st != MOE_OK) return st;
+  if (!known_dtype(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (n_rows == 0) return MOE_OK;
+  if (!xq || !x_scale || !group_offsets || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned4(x_scale) || !aligned4(group_offsets) || !aligned16(w) || !aligned16(w_scale) ||
+      !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (x_rows && (!aligned4(x_rows) || n_x < 1)) return MOE_ERR_INVALID_ARG;
+  if (x_rows && !fits_int(static_cast<long long>(n_x) * K)) return MOE_ERR_UNSUPPORTED;
+  moe::GroupedI8 g{x_rows, x_rows ? n_x : n_rows, group_offsets, n_rows, E, n_shared, nseg};
+  return hip_status(
+      moe::launch_grouped_linear_i8(g, xq, x_scale, K, O, w, w_scale, out_dtype == MOE_BF16 ? 1 : 0, y, stream));
+}
+
+moe_status moe_grouped_ffn_i8(const void* x_sorted, const int32_t* x_rows, int32_t n_x,
+                              const int32_t* group_offsets, int32_t n_rows, int32_t E, int32_t n_shared,
+                              int32_t nseg, int32_t d, int32_t I, const int8_t* w_gate, const float* s_gate,
+                              const int8_t* w_up, const float* s_up, const int8_t* w_down, const float* s_down,
+                              void* h_sorted, void* workspace, size_t* workspace_bytes, hipStream_t stream) {
+  moe_status st = grouped_i8_sizes(n_rows, E, n_shared, nseg, d, I);
+  if (st != MOE_OK) return st;
+  if (n_x < 0) return MOE_ERR_INVALID_ARG;
+  if (!fits_int(static_cast<long long>(n_x) * d)) return MOE_ERR_UNSUPPORTED;
+  // a query has no row list to look at: n_x > 0 stands for one
+  const int32_t tokens = workspace == nullptr ? (n_x > 0 ? n_x : n_rows) : (x_rows ? n_x : n_rows);
+  bool query;
+  st = workspace_check(workspace, workspace_bytes, moe::ffn_i8_workspace_bytes(n_rows, tokens, d, I), &query);
+  if (st != MOE_OK || query) return st;
+  if (n_rows == 0) return MOE_OK;
+  if (!x_sorted || !group_offsets || !w_gate || !w_up || !w_down || !s_gate || !s_up || !s_down || !h_sorted)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x_sorted) || !aligned4(group_offsets) || !aligned16(w_gate) || !aligned16(w_up) ||
+      !aligned16(w_down) || !aligned16(s_gate) || !aligned16(s_up) || !aligned16(s_down) || !aligned16(h_sorted))
+    return MOE_ERR_INVALID_ARG;
+  if (x_rows && (!aligned4(x_rows) || n_x < 1)) return MOE_ERR_INVALID_ARG;
+  moe::FfnI8Args a;
+  a.g = moe::GroupedI8{x_rows, tokens, group_offsets, n_rows, E, n_shared, nseg};
+  a.x = x_sorted;
+  a.d = d;
+  a.I = I;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.w_down = w_down;
+  a.s_gate = s_gate;
+  a.s_up = s_up;
+  a.s_down = s_down;
+  a.h_sorted = h_sorted;
+  return hip_status(moe::launch_ffn_i8(a, workspace, stream));
+}
 
 moe_status moe_prob_signature(const float* logits, int32_t L, int32_t T, int32_t E, const int32_t* req_offsets,
                               int32_t R, float* signature, hipStream_t stream) {

@@ -15,6 +15,20 @@ hipError_t launch_gate_record(const float* logits, int T, int E, int k, int reno
                               float* topk_w, int block_tokens, int layer, int L, int* block_counts,
                               hipStream_t stream);
 
+// ---- routing with scores -----------------------------------------------------
+struct RouteArgs {
+  int T, E, k;
+  int bf16;      // logits: 1 bf16, 0 fp32
+  int sigmoid;   // 0: softmax
+  int n_groups, top_groups;
+  int top2;      // group value: sum of the two best, 0: the best
+  int renormalize;
+  float scale;
+  int* topk_ids;
+  float* topk_w;
+};
+hipError_t launch_route(const void* logits, const float* bias, const RouteArgs& a, hipStream_t stream);
+
 // ---- router projection -------------------------------------------------------
 hipError_t launch_router(const void* x, const void* w_router, int T, int d, int E, int bf16, float* logits,
                          hipStream_t stream);
@@ -77,6 +91,29 @@ size_t ffn_fp8w_workspace_bytes(int n_rows, int E, int n_shared, int nseg, int d
 bool fp8w_uses_gemm(int n_rows, int G, int d, int I, bool packed, const void* s_gate, const void* s_up,
                     const void* s_down);
 hipError_t launch_ffn_fp8w(const FfnArgs& a, void* workspace, hipStream_t stream);
+
+// ---- int8 rows and products ----------------------------------------------------
+hipError_t launch_quantize_rows(const void* x, int bf16, int T, int d, int8_t* q, float* s, hipStream_t stream);
+
+struct GroupedI8 {
+  const int* x_rows;   // nullptr: sorted row n reads row n
+  int n_x;
+  const int* group_offsets;
+  int n_rows, E, n_shared, nseg;
+};
+// y[n][o], packed int8 weights [E+S][O][K]; bf16: output type
+hipError_t launch_grouped_linear_i8(const GroupedI8& g, const int8_t* xq, const float* xs, int K, int O,
+                                    const int8_t* w, const float* ws, int bf16, void* y, hipStream_t stream);
+struct FfnI8Args {
+  GroupedI8 g;
+  const void* x;       // bf16 tokens
+  int d, I;
+  const int8_t *w_gate, *w_up, *w_down;
+  const float *s_gate, *s_up, *s_down;
+  void* h_sorted;
+};
+size_t ffn_i8_workspace_bytes(int n_rows, int n_tokens, int d, int I);
+hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream);
 
 // ---- combine ---------------------------------------------------------------
 hipError_t launch_combine(const void* h_sorted, const int* flat_to_sorted, const float* topk_w, int T,
