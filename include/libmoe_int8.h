@@ -7,7 +7,8 @@
  *
  * Quantisation, the same everywhere: of a row of values v (a token's hidden
  * state, or 128 columns of the SwiGLU product)
- *     scale = max |v| / 127 in fp32 (correctly rounded; 1 where it is 0)
+ *     scale = max |v| * c in fp32, c the fp32 number nearest to 1 / 127 (1 where the
+ *             product is 0)
  *     code  = v / scale rounded to the nearest integer, halves to even, the
  *             quotient exact, held to [-127, 127].
  * Values that are not all finite give the scale NaN and codes 0, so that what is

@@ -54,7 +54,7 @@ def quantize(v):
         if not np.all(np.isfinite(row)):
             s[r] = np.nan
             continue
-        a = np.float32(np.abs(row).max()) / np.float32(127.0) if row.size else np.float32(0)
+        a = np.float32(np.abs(row).max()) * (np.float32(1.0) / np.float32(127.0))
         s[r] = a if a > 0 else np.float32(1.0)
         q[r] = np.clip(np.rint(row / np.float64(s[r])), -127, 127).astype(np.int64)
     return q.reshape(v.shape), s.reshape(v.shape[:-1])

@@ -517,7 +517,7 @@ def grouped_ffn_fp8w(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_sha
 
 def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None):
     """int8 codes [..][d] and fp32 scales [..] of the rows of x [..][d] (bf16 or
-    fp32): scale = max|row| / 127, codes to the nearest, halves to even
+    fp32): scale = max|row| * fl(1/127), codes to the nearest, halves to even
     (moe_quantize_rows_i8).  Serves token rows and, once, weights."""
     _need(x, "x")
     if x.dim() < 1:

@@ -287,11 +287,405 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_i8(ProductArgs p) {
   }
 }
 
+// ---- large groups: LDS-tiled products ----------------------------------------------
+// A persistent block (one per CU) walks its list of tiles: BM rows x 256 weight rows
+// (kGateUp: 128 gate and the same 128 up rows).  K advances 64 codes a step through a
+// ring of LDS stages that LDS-DMA loads fill ahead; the steps of all tiles form one
+// stream, so the next tile's first steps load while this one finishes.
+//   * rows: 64 bytes of a row per step, four 16-byte pieces; piece c of row r lies at slot
+//     c ^ swz(r), so that the 16 rows of an operand read hit different banks.  A DMA
+//     instruction fills 16 rows (lane -> row lane / 4, slot lane % 4).
+//   * weights: a packed block (16 rows x 64 codes, 1 KiB) is copied as it is.
+//   * what the epilogue and the next tile need from memory (the row list, the rows' and
+//     the channels' scales) comes by DMA too, a tile ahead, because a load that the
+//     compiler sees would make it wait for everything in flight.
+// Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave,
+// so the rows of a partial tile spread over them.
+template <int MI_, int NJ_, int WM_, int WN_>
+struct TileCfg {
+  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = kWave * NW;
+  static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
+  static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;
+  static_assert(BN == 2 * kBlock, "a tile holds the columns of one scale");
+  static_assert(ADMA >= 1 && ADMA <= 4 && BDMA >= 1, "DMA instructions per wave");
+};
+template <class C, Mode M>
+struct TileLds {
+  static constexpr int SUB = M == kDown ? 2 : 1;               // K steps per stage
+  static constexpr int STAGES = M == kDown ? 2 : 4;
+  static constexpr int A = C::BM * kStep, B = C::BN * kStep;   // bytes per K step
+  static constexpr int ROWS = C::NW * kWave * 4;               // one 4-byte value per row slot
+  static constexpr int STAGE = SUB * (A + B) + (M == kDown ? ROWS : 0);
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int LIST = RING;                            // row list of two tiles
+  static constexpr int SA = LIST + 2 * ROWS;                   // row scales of two tiles
+  static constexpr int SB = SA + 2 * ROWS;                     // channel scales of two tiles
+  static constexpr int MAX = SB + 2 * 1024;                    // kGateUp: largest magnitudes
+  static constexpr int PLAN = MAX + C::WN * C::BM * 4;         // tiles before each group, group offsets
+  static int bytes(int G) { return PLAN + 8 * (G + 1); }
+};
+
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+
+// LDS-DMA loads: each lane's 16 or 4 bytes go to LDS address lds + 16 (or 4) * lane.
+// Inline assembly, so that the compiler does not wait for them before every LDS
+// read; the waits are explicit.  M0 holds the LDS base and needs one wait state.
+__device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+// At most `ahead` stages of PER loads may still be in flight (loads complete in order).
+template <int PER, int MAXA>
+__device__ __forceinline__ void wait_stage(int ahead) {
+  if constexpr (MAXA == 0) {
+    wait_loads_barrier<0>();
+  } else {
+    if (ahead >= MAXA) wait_loads_barrier<MAXA * PER>();
+    else wait_stage<PER, MAXA - 1>(ahead);
+  }
+}
+// LDS writes of all waves before LDS reads of all waves, DMA loads left in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) const uint8_t lds_byte;
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)p));
+}
+
+__device__ __forceinline__ Item uniform(const Item& i) {
+  return Item{__builtin_amdgcn_readfirstlane(i.row0),   __builtin_amdgcn_readfirstlane(i.rows),
+              __builtin_amdgcn_readfirstlane(i.expert), __builtin_amdgcn_readfirstlane(i.chunk),
+              __builtin_amdgcn_readfirstlane(i.split),  __builtin_amdgcn_readfirstlane(i.row1)};
+}
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
+template <class C, Mode M, class Out>
+__global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
+  using L = TileLds<C, M>;
+  constexpr int MI = C::MI, NJ = C::NJ, WM = C::WM, WN = C::WN, NW = C::NW, NT = C::NT, BM = C::BM;
+  constexpr int OUTC = M == kGateUp ? C::BN / 2 : C::BN;
+  constexpr int GPT = (kMaxGroups + NT - 1) / NT;
+  constexpr int kPanel = 4;                                    // column chunks that follow each other per m-tile
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  int* before = reinterpret_cast<int*>(lds + L::PLAN);         // m-tiles before group g
+  int* offs = before + p.G + 1;
+  __shared__ int wsum[NW];
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+  const int K = p.K, cols = p.cols;
+
+  for (int g = tid; g <= p.G; g += NT) offs[g] = p.offs[g];
+  __syncthreads();
+  {
+    int cnt[GPT], sum = 0;
+#pragma unroll
+    for (int i = 0; i < GPT; ++i) {
+      const int g = tid * GPT + i;
+      cnt[i] = g < p.G ? group_rows(offs, p.n_rows, p.E, p.nseg, BM, g).nt : 0;
+      sum += cnt[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int y = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += y;
+    }
+    if (lane == kWave - 1) wsum[wave] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int i = 0; i < wave; ++i) run += wsum[i];
+#pragma unroll
+    for (int i = 0; i < GPT; ++i) {
+      const int g = tid * GPT + i;
+      if (g < p.G) before[g] = run;
+      run += cnt[i];
+    }
+    if (tid == NT - 1) before[p.G] = run;
+    __syncthreads();
+  }
+  // XCD x (blocks are dealt round-robin) owns the x-th eighth of the list of tiles, so
+  // that tiles which share weights or rows run in one L2; its blocks take them in turn
+  const int nch = (cols + OUTC - 1) / OUTC;
+  const int items = __builtin_amdgcn_readfirstlane(before[p.G]) * nch;
+  const int per_xcd = static_cast<int>(gridDim.x) / kXcds;
+  const int share = (items + kXcds - 1) / kXcds;
+  const int first = static_cast<int>(blockIdx.x % kXcds) * share + static_cast<int>(blockIdx.x / kXcds);
+  const int end = min(items, static_cast<int>(blockIdx.x % kXcds + 1) * share);
+  const int n_my = first < end ? (end - first - 1) / per_xcd + 1 : 0;
+  if (n_my == 0) return;
+  auto item_of = [&](int i) -> Item {
+    const int want = first + i * per_xcd;
+    const int u = want / nch;
+    int lo = 0, hi = p.G;                                      // last g with before[g] <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= u) lo = mid; else hi = mid;
+    }
+    const int nt = before[lo + 1] - before[lo];
+    const int local = want - before[lo] * nch;
+    const int panel = local / (kPanel * nt), rest = local - panel * kPanel * nt;
+    const int pc = min(kPanel, nch - panel * kPanel);
+    return uniform(group_tile(group_rows(offs, p.n_rows, p.E, p.nseg, BM, lo), lo, rest / pc, panel * kPanel + rest % pc,
+                              BM, p.E, p.nseg));
+  };
+
+  // ---- issue side
+  const uint32_t lds0 = lds_address(lds);
+  const int nsteps = K / kStep, nk = (nsteps + L::SUB - 1) / L::SUB;
+  const int total = n_my * nk;
+  const int8_t* ap[C::ADMA];
+  const int8_t* bp[C::BDMA];
+  const float* sp = nullptr;                                   // kDown: this lane's row's block scales
+  // this lane's row in 4-byte loads of one value per row: slots of wave w are [64 w, 64 w + 64)
+  const int vrow = 16 * (wave + NW * min(lane >> 4, C::ADMA - 1)) + l16;
+  auto list_ahead = [&](const Item& it, int parity) {
+    if (p.x_rows) dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * 256);
+  };
+  Item nxt = item_of(0), isd = nxt;                            // tile issued next, issued now
+  int ir = 0, ikt = 0, islot = 0;
+  auto begin_tile = [&]() {
+    const int par = ir & 1;
+    isd = nxt;
+    const int* list = reinterpret_cast<const int*>(lds + L::LIST + par * L::ROWS) + wave * 64;
+    auto src = [&](int r, int slot) {
+      return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : isd.row(min(r, isd.rows - 1));
+    };
+#pragma unroll
+    for (int i = 0; i < C::ADMA; ++i) {
+      const int r = 16 * (wave + NW * i) + (lane >> 2);
+      ap[i] = p.a + static_cast<size_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
+    }
+    const int n0 = isd.chunk * OUTC;
+    const size_t e0 = static_cast<size_t>(isd.expert) * cols;
+#pragma unroll
+    for (int i = 0; i < C::BDMA; ++i) {
+      const int b = wave + NW * i;                             // 16-row block of the tile
+      const bool up = M == kGateUp && b >= C::BN / 32;
+      const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
+      bp[i] = (up ? p.w1 : p.w0) + (e0 + n) * K + lane * 16;
+    }
+    if (wave == 0) {
+      const bool up = M == kGateUp && lane >= 32;
+      const int n = min(n0 + 4 * (M == kGateUp ? lane & 31 : lane), cols - 4);
+      dma16((up ? p.s1 : p.s0) + e0 + n, lds0 + L::SB + par * 1024);
+    }
+    if constexpr (M == kDown) sp = p.as + isd.row(min(vrow, isd.rows - 1));
+    else dma4(p.as + src(vrow, min(lane, 16 * C::ADMA - 1)), lds0 + L::SA + par * L::ROWS + wave * 256);
+    if (ir + 1 < n_my) {
+      nxt = item_of(ir + 1);
+      list_ahead(nxt, par ^ 1);
+    }
+  };
+  auto issue = [&]() {
+    if (ikt == 0) begin_tile();
+    const uint32_t st = lds0 + islot * L::STAGE + wave * 1024;
+    if constexpr (M == kDown)
+      dma4(sp + static_cast<size_t>(ikt) * p.n_rows, lds0 + islot * L::STAGE + L::SUB * (L::A + L::B) + wave * 256);
+#pragma unroll
+    for (int s = 0; s < L::SUB; ++s) {
+      const int kt = min(ikt * L::SUB + s, nsteps - 1);        // the step past an odd end is loaded, not used
+#pragma unroll
+      for (int i = 0; i < C::ADMA; ++i) dma16(ap[i] + kt * kStep, st + s * L::A + i * NW * 1024);
+#pragma unroll
+      for (int i = 0; i < C::BDMA; ++i) dma16(bp[i] + static_cast<size_t>(kt) * 1024, st + L::SUB * L::A + s * L::B + i * NW * 1024);
+    }
+    islot = islot + 1 == L::STAGES ? 0 : islot + 1;
+    if (++ikt == nk) {
+      ikt = 0;
+      ++ir;
+    }
+  };
+  list_ahead(nxt, 0);
+  wait_loads_barrier<0>();
+#pragma unroll
+  for (int s = 0; s < L::STAGES - 1; ++s)
+    if (s < total) issue();
+
+  // ---- compute side
+  const int aoff = 16 * wm * kStep + l16 * kStep + 16 * (q ^ swz(l16));   // 16-row blocks do not change swz
+  int gs = 0, cslot = 0;
+  constexpr int PER = L::SUB * (C::ADMA + C::BDMA);
+  for (int cr = 0; cr < n_my; ++cr) {
+    const Item it = item_of(cr);
+    const int par = cr & 1;
+    i32x4 acc[M == kDown ? 1 : MI][M == kDown ? 1 : NJ];
+    f32x4 facc[M == kDown ? MI : 1][M == kDown ? NJ : 1];
+    if constexpr (M == kDown) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) facc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    } else {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    }
+    const int blocks = (it.rows + 15) >> 4;                    // 16-row blocks with rows
+    const int nv = max(0, (blocks - wm + WM - 1) / WM);        // of them this wave's
+    auto loop = [&](auto nvc) {
+      constexpr int NV = decltype(nvc)::value;
+      for (int kt = 0; kt < nk; ++kt, ++gs) {
+        wait_stage<PER, L::STAGES - 2>(min(L::STAGES - 2, total - 1 - gs));
+        if (gs + L::STAGES - 1 < total) issue();               // every wave is past stage gs - 1
+        const uint8_t* st = lds + cslot * L::STAGE;
+        cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
+        auto bfrag = [&](int s, int j) {
+          const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2)
+                                     : wn * NJ + j;
+          return *reinterpret_cast<const uint4*>(st + L::SUB * L::A + s * L::B + b * 1024 + lane * 16);
+        };
+        auto afrag = [&](int s, int i) {
+          return *reinterpret_cast<const uint4*>(st + s * L::A + aoff + 16 * WM * i * kStep);
+        };
+        if constexpr (M == kDown) {
+          const bool two = 2 * kt + 1 < nsteps;
+          uint4 b0[NJ], b1[NJ];
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            b0[j] = bfrag(0, j);
+            b1[j] = two ? bfrag(1, j) : make_uint4(0, 0, 0, 0);
+          }
+          const float* sc = reinterpret_cast<const float*>(st + L::SUB * (L::A + L::B));
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const uint4 a0 = afrag(0, i), a1 = afrag(1, i);
+            const int blk = wm + WM * i;
+            const float s = sc[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const i32x4 t = mfma_i8(b1[j], a1, mfma_i8(b0[j], a0, i32x4{0, 0, 0, 0}));
+#pragma unroll
+              for (int r = 0; r < 4; ++r) facc[i][j][r] = __builtin_fmaf(static_cast<float>(t[r]), s, facc[i][j][r]);
+            }
+          }
+        } else {
+          uint4 b[NJ];
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) b[j] = bfrag(0, j);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const uint4 a = afrag(0, i);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_i8(b[j], a, acc[i][j]);
+          }
+        }
+      }
+    };
+    if (nv > MI / 2) loop(Int<MI>{});
+    else if (nv > MI / 4) loop(Int<MI / 2>{});
+    else loop(Int<MI / 4>{});
+
+    // ---- epilogue
+    const float* sa = reinterpret_cast<const float*>(lds + L::SA + par * L::ROWS);
+    const float* sb = reinterpret_cast<const float*>(lds + L::SB + par * 1024);
+    const int n0 = it.chunk * OUTC;
+    if constexpr (M == kGateUp) {
+      uint32_t* mx = reinterpret_cast<uint32_t*>(lds + L::MAX);
+      float v[MI][NJ / 2][4];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int blk = wm + WM * i;
+        const float sx = sa[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+        uint32_t big = 0;
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+          const int c = 16 * (wn * (NJ / 2) + j) + 4 * q;
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(sb + c), w1 = *reinterpret_cast<const f32x4*>(sb + 128 + c);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v[i][j][r] = silu_mul(static_cast<float>(acc[i][j][r]) * (sx * w0[r]),
+                                  static_cast<float>(acc[i][NJ / 2 + j][r]) * (sx * w1[r]));
+            if (n0 + c < cols) big = max(big, abs_bits(v[i][j][r]));
+          }
+        }
+        big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 16, kWave)));
+        big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 32, kWave)));
+        if (q == 0) mx[wn * BM + 16 * blk + l16] = big;
+      }
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = 16 * (wm + WM * i) + l16;
+        if (m >= it.rows) continue;
+        uint32_t big = mx[m];
+#pragma unroll
+        for (int w = 1; w < WN; ++w) big = max(big, mx[w * BM + m]);
+        const QuantScale qs = quant_scale(big);
+        const int row = it.row(m);
+        if (wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.scale;
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+          const int n = n0 + 16 * (wn * (NJ / 2) + j) + 4 * q;
+          if (n < cols)
+            *reinterpret_cast<uint32_t*>(static_cast<int8_t*>(p.out) + static_cast<size_t>(row) * cols + n) =
+                pack_codes(quant_code(v[i][j][0], qs), quant_code(v[i][j][1], qs), quant_code(v[i][j][2], qs),
+                           quant_code(v[i][j][3], qs));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int blk = wm + WM * i, m = 16 * blk + l16;
+        if (m >= it.rows) continue;
+        float sx = 1.f;
+        if constexpr (M == kLinear) sx = sa[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+        Out* orow = static_cast<Out*>(p.out) + static_cast<size_t>(it.row(m)) * cols;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int c = 16 * (wn * NJ + j) + 4 * q;
+          if (n0 + c >= cols) continue;
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(sb + c);
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (M == kDown) v[r] = facc[i][j][r] * w0[r];
+            else v[r] = static_cast<float>(acc[i][j][r]) * (sx * w0[r]);
+          }
+          store4(orow + n0 + c, v);
+        }
+      }
+    }
+  }
+}
+
 int pick_mf(int avg) { return avg <= 12 ? 1 : avg <= 28 ? 2 : 4; }
+
+// CUs of the current device.
+int device_cus() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return 256;
+  return cus;
+}
+
+#ifndef I8_CFG
+#define I8_CFG TileCfg<8, 8, 2, 2>
+#endif
+using Tile = I8_CFG;
+constexpr int kTileMinAvg = 48;
+constexpr int kTileMinK = 4 * kStep;   // the row list of a tile is loaded a tile ahead: at least STAGES - 1 steps
 
 template <Mode M, class Out>
 void launch_product(const ProductArgs& p, hipStream_t stream) {
   const int avg = p.n_rows / p.G;
+  if (avg > kTileMinAvg && p.K >= kTileMinK) {
+    const int grid = (device_cus() + kXcds - 1) / kXcds * kXcds;
+    const size_t lds = TileLds<Tile, M>::bytes(p.G);
+    hipLaunchKernelGGL((tile_i8<Tile, M, Out>), dim3(grid), dim3(Tile::NT), lds, stream, p);
+    return;
+  }
   const int mf = pick_mf(avg);
   const int max_tiles = (p.n_rows + 16 * mf - 1) / (16 * mf) + p.G;
   dim3 grid(item_grid(max_tiles, (p.cols + kBlock - 1) / kBlock)), block(kThreadsS);
@@ -367,6 +761,8 @@ hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream
   p.out_scale = reinterpret_cast<float*>(ws + L.as);
   launch_product<kGateUp, int8_t>(p, stream);
   ProductArgs h = product_args(a.g, a.I, a.d);
+  h.x_rows = nullptr;                       // the SwiGLU product is in sorted order
+  h.n_x = a.g.n_rows;
   h.a = reinterpret_cast<const int8_t*>(ws + L.aq);
   h.as = p.out_scale;
   h.w0 = a.w_down;

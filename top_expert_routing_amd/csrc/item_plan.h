@@ -86,15 +86,19 @@ MOE_HD int group_items(const GroupRows& r, int g, int nch, int x) {
   return r.nt * xcd_chunks(xcd_first_chunk(g, nch, x), nch);
 }
 
-// The `local`-th of those items (0 <= local < group_items).
-MOE_HD Item group_item(const GroupRows& r, int g, int nch, int x, int local, int BM, int E, int nseg) {
-  const int j = xcd_first_chunk(g, nch, x) + kXcds * (local / r.nt);
-  const int a = (r.t0 + local % r.nt) * BM;                  // first row of the tile in the sequence
+// m-tile `mt` (0 <= mt < r.nt) of group g against column chunk j.
+MOE_HD Item group_tile(const GroupRows& r, int g, int mt, int j, int BM, int E, int nseg) {
+  const int a = (r.t0 + mt) * BM;                            // first row of the tile in the sequence
   const int left = r.na + r.nb - a;
   const int rows = left < BM ? left : BM;
   const int sp = r.na - a;
   const int split = sp < 0 ? 0 : (sp > rows ? rows : sp);
   return Item{r.a0 + a, rows, group_expert(g, E, nseg), j, split, r.b0 + (a > r.na ? a - r.na : 0)};
+}
+
+// The `local`-th of those items (0 <= local < group_items).
+MOE_HD Item group_item(const GroupRows& r, int g, int nch, int x, int local, int BM, int E, int nseg) {
+  return group_tile(r, g, local % r.nt, xcd_first_chunk(g, nch, x) + kXcds * (local / r.nt), BM, E, nseg);
 }
 
 // Grid size that covers every possible item of a call: XCD x holds at most

@@ -1,5 +1,5 @@
 // int8 quantisation shared by the row quantiser and the FFN's epilogue:
-//   scale = max |v| / 127 (fp32, correctly rounded; 1 for 0; NaN unless all v are finite)
+//   scale = max |v| * fl(1 / 127) in fp32 (1 where that is 0; NaN unless all v are finite)
 //   code  = RNE(v / scale), the quotient exact, held to [-127, 127].
 #pragma once
 
@@ -21,7 +21,7 @@ __device__ __forceinline__ QuantScale quant_scale(uint32_t amax_bits) {
   QuantScale q;
   const float amax = __uint_as_float(amax_bits);
   const bool finite = amax_bits < 0x7f800000u;
-  float s = amax / 127.0f;
+  float s = amax * (1.0f / 127.0f);
   if (s == 0.0f) s = 1.0f;
   q.up = s < 0x1p-90f ? 0x1p64f : 1.0f;
   q.scale = finite ? s : __builtin_nanf("");
