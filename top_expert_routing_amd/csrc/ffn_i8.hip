@@ -31,6 +31,9 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// Lambdas over the kernel's state: a call that is not inlined would put that state in memory.
+#define MOE_INLINE __attribute__((always_inline))
+
 enum Mode { kLinear, kGateUp, kDown };
 
 constexpr int kBlock = 128;          // columns of the SwiGLU product that share a scale
@@ -313,6 +316,7 @@ template <class C, Mode M>
 struct TileLds {
   static constexpr int SUB = M == kDown ? 2 : 1;               // K steps per stage
   static constexpr int STAGES = M == kDown ? 2 : 4;
+  static constexpr int AHEAD = M == kDown ? 1 : 3;             // stages requested before the first is used
   static constexpr int A = C::BM * kStep, B = C::BN * kStep;   // bytes per K step
   static constexpr int ROWS = C::NW * kWave * 4;               // one 4-byte value per row slot
   static constexpr int STAGE = SUB * (A + B) + (M == kDown ? ROWS : 0);
@@ -329,26 +333,27 @@ __device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
 
 // LDS-DMA loads: each lane's 16 or 4 bytes go to LDS address lds + 16 (or 4) * lane.
 // Inline assembly, so that the compiler does not wait for them before every LDS
-// read; the waits are explicit.  M0 holds the LDS base and needs one wait state.
+// read; the waits are explicit.  M0 holds the LDS base; s_nop as below.
 __device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+}
+// The same from a wave-uniform address plus a lane's 32-bit offset.  The address may have
+// been put into its scalar registers by a vector instruction (a readfirstlane, or a
+// v_readlane from the register a spilled scalar is kept in) just before; a vector memory
+// instruction may use it five wait states later, and the compiler does not look for that
+// hazard inside inline assembly: s_nop 4.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32))) << 32 |
+                     static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(u), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads_barrier() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
-}
-// At most `ahead` stages of PER loads may still be in flight (loads complete in order).
-template <int PER, int MAXA>
-__device__ __forceinline__ void wait_stage(int ahead) {
-  if constexpr (MAXA == 0) {
-    wait_loads_barrier<0>();
-  } else {
-    if (ahead >= MAXA) wait_loads_barrier<MAXA * PER>();
-    else wait_stage<PER, MAXA - 1>(ahead);
-  }
 }
 // LDS writes of all waves before LDS reads of all waves, DMA loads left in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
@@ -363,11 +368,6 @@ __device__ __forceinline__ Item uniform(const Item& i) {
               __builtin_amdgcn_readfirstlane(i.expert), __builtin_amdgcn_readfirstlane(i.chunk),
               __builtin_amdgcn_readfirstlane(i.split),  __builtin_amdgcn_readfirstlane(i.row1)};
 }
-
-template <int V>
-struct Int {
-  static constexpr int value = V;
-};
 
 template <class C, Mode M, class Out>
 __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
@@ -423,7 +423,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
   const int end = min(items, static_cast<int>(blockIdx.x % kXcds + 1) * share);
   const int n_my = first < end ? (end - first - 1) / per_xcd + 1 : 0;
   if (n_my == 0) return;
-  auto item_of = [&](int i) -> Item {
+  auto item_of = [&](int i) MOE_INLINE -> Item {
     const int want = first + i * per_xcd;
     const int u = want / nch;
     int lo = 0, hi = p.G;                                      // last g with before[g] <= u
@@ -439,85 +439,121 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
                               BM, p.E, p.nseg));
   };
 
-  // ---- issue side
+  // ---- the loads, STAGES - 1 steps ahead of the products
   const uint32_t lds0 = lds_address(lds);
-  const int nsteps = K / kStep, nk = (nsteps + L::SUB - 1) / L::SUB;
-  const int total = n_my * nk;
-  const int8_t* ap[C::ADMA];
-  const int8_t* bp[C::BDMA];
-  const float* sp = nullptr;                                   // kDown: this lane's row's block scales
+  const int nsteps = K / kStep, nk = (nsteps + L::SUB - 1) / L::SUB;   // K steps and stages of a tile
+  uint32_t ao[C::ADMA], ao_next[C::ADMA];                      // this lane's bytes from p.a: tile being loaded, tile after it
+  const int8_t *bp[C::BDMA], *bp_next[C::BDMA];                // wave-uniform
+  const float *sp = nullptr, *sp_next = nullptr;               // kDown: this lane's row's block scales
   // this lane's row in 4-byte loads of one value per row: slots of wave w are [64 w, 64 w + 64)
   const int vrow = 16 * (wave + NW * min(lane >> 4, C::ADMA - 1)) + l16;
-  auto list_ahead = [&](const Item& it, int parity) {
+  auto load_list = [&](const Item& it, int parity) MOE_INLINE {
     if (p.x_rows) dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * 256);
   };
-  Item nxt = item_of(0), isd = nxt;                            // tile issued next, issued now
-  int ir = 0, ikt = 0, islot = 0;
-  auto begin_tile = [&]() {
-    const int par = ir & 1;
-    isd = nxt;
-    const int* list = reinterpret_cast<const int*>(lds + L::LIST + par * L::ROWS) + wave * 64;
-    auto src = [&](int r, int slot) {
-      return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : isd.row(min(r, isd.rows - 1));
+  // Sources of a tile whose row list has arrived; requests its scales.
+  auto aim = [&](const Item& it, int parity) MOE_INLINE {
+    const int* list = reinterpret_cast<const int*>(lds + L::LIST + parity * L::ROWS) + wave * 64;
+    auto src = [&](int r, int slot) MOE_INLINE {
+      return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : it.row(min(r, it.rows - 1));
     };
 #pragma unroll
     for (int i = 0; i < C::ADMA; ++i) {
       const int r = 16 * (wave + NW * i) + (lane >> 2);
-      ap[i] = p.a + static_cast<size_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
+      ao_next[i] = static_cast<uint32_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
     }
-    const int n0 = isd.chunk * OUTC;
-    const size_t e0 = static_cast<size_t>(isd.expert) * cols;
+    const int n0 = it.chunk * OUTC;
+    const size_t e0 = static_cast<size_t>(it.expert) * cols;
 #pragma unroll
     for (int i = 0; i < C::BDMA; ++i) {
       const int b = wave + NW * i;                             // 16-row block of the tile
       const bool up = M == kGateUp && b >= C::BN / 32;
       const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
-      bp[i] = (up ? p.w1 : p.w0) + (e0 + n) * K + lane * 16;
+      bp_next[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
     }
     if (wave == 0) {
       const bool up = M == kGateUp && lane >= 32;
       const int n = min(n0 + 4 * (M == kGateUp ? lane & 31 : lane), cols - 4);
-      dma16((up ? p.s1 : p.s0) + e0 + n, lds0 + L::SB + par * 1024);
+      dma16((up ? p.s1 : p.s0) + e0 + n, lds0 + L::SB + parity * 1024);
     }
-    if constexpr (M == kDown) sp = p.as + isd.row(min(vrow, isd.rows - 1));
-    else dma4(p.as + src(vrow, min(lane, 16 * C::ADMA - 1)), lds0 + L::SA + par * L::ROWS + wave * 256);
-    if (ir + 1 < n_my) {
-      nxt = item_of(ir + 1);
-      list_ahead(nxt, par ^ 1);
-    }
+    if constexpr (M == kDown) sp_next = p.as + it.row(min(vrow, it.rows - 1));
+    else dma4(p.as + src(vrow, min(lane, 16 * C::ADMA - 1)), lds0 + L::SA + parity * L::ROWS + wave * 256);
   };
-  auto issue = [&]() {
-    if (ikt == 0) begin_tile();
+  int ikt = 0, islot = 0;                                      // the stage requested next: of its tile, ring slot
+  auto turn = [&]() MOE_INLINE {                               // go on with the next tile
+    ikt = 0;
+#pragma unroll
+    for (int i = 0; i < C::ADMA; ++i) ao[i] = ao_next[i];
+#pragma unroll
+    for (int i = 0; i < C::BDMA; ++i) bp[i] = bp_next[i];
+    sp = sp_next;
+  };
+  constexpr int PER = L::SUB * (C::ADMA + C::BDMA);            // loads of a stage per wave (kDown: and one of scales)
+  auto load = [&](int i) MOE_INLINE {                          // the i-th of them
+    const int s = i / (C::ADMA + C::BDMA), n = i % (C::ADMA + C::BDMA);
+    const int kt = min(ikt * L::SUB + s, nsteps - 1);          // steps past K: loaded again, not used
     const uint32_t st = lds0 + islot * L::STAGE + wave * 1024;
+    if (n < C::ADMA) dma16(p.a + kt * kStep, ao[n], st + s * L::A + n * NW * 1024);
+    else dma16(bp[n - C::ADMA] + static_cast<size_t>(kt) * 1024, lane * 16, st + L::SUB * L::A + s * L::B + (n - C::ADMA) * NW * 1024);
+  };
+  // kLinear, kGateUp take K steps in pairs (two register sets), an odd last one with an empty step
+  const int stages = M == kDown ? nk : (nk + 1) & ~1;
+  auto loaded = [&]() MOE_INLINE {
+    islot = islot + 1 == L::STAGES ? 0 : islot + 1;
+    if (++ikt == stages) turn();
+  };
+  auto load_scales = [&]() MOE_INLINE {
     if constexpr (M == kDown)
       dma4(sp + static_cast<size_t>(ikt) * p.n_rows, lds0 + islot * L::STAGE + L::SUB * (L::A + L::B) + wave * 256);
-#pragma unroll
-    for (int s = 0; s < L::SUB; ++s) {
-      const int kt = min(ikt * L::SUB + s, nsteps - 1);        // the step past an odd end is loaded, not used
-#pragma unroll
-      for (int i = 0; i < C::ADMA; ++i) dma16(ap[i] + kt * kStep, st + s * L::A + i * NW * 1024);
-#pragma unroll
-      for (int i = 0; i < C::BDMA; ++i) dma16(bp[i] + static_cast<size_t>(kt) * 1024, st + L::SUB * L::A + s * L::B + i * NW * 1024);
-    }
-    islot = islot + 1 == L::STAGES ? 0 : islot + 1;
-    if (++ikt == nk) {
-      ikt = 0;
-      ++ir;
-    }
   };
-  list_ahead(nxt, 0);
+  Item cur = item_of(0), nxt = n_my > 1 ? item_of(1) : cur;
+  load_list(cur, 0);
+  load_list(nxt, 1);
   wait_loads_barrier<0>();
+  aim(cur, 0);
+  turn();
+#pragma unroll 1
+  for (int s = 0; s < L::AHEAD; ++s) {                         // stages >= AHEAD (checked by the host)
+    load_scales();
 #pragma unroll
-  for (int s = 0; s < L::STAGES - 1; ++s)
-    if (s < total) issue();
+    for (int i = 0; i < PER; ++i) load(i);
+    loaded();
+  }
 
   // ---- compute side
   const int aoff = 16 * wm * kStep + l16 * kStep + 16 * (q ^ swz(l16));   // 16-row blocks do not change swz
-  int gs = 0, cslot = 0;
-  constexpr int PER = L::SUB * (C::ADMA + C::BDMA);
+  int cslot = 0;
+  auto next_stage = [&]() MOE_INLINE {
+    const uint8_t* st = lds + cslot * L::STAGE;
+    cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
+    return st;
+  };
+  auto bfrag = [&](const uint8_t* st, int s, int j) MOE_INLINE {
+    const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2) : wn * NJ + j;
+    return *reinterpret_cast<const uint4*>(st + L::SUB * L::A + s * L::B + b * 1024 + lane * 16);
+  };
+  auto afrag = [&](const uint8_t* st, int s, int i) MOE_INLINE {
+    return *reinterpret_cast<const uint4*>(st + s * L::A + aoff + 16 * WM * i * kStep);
+  };
+  // kLinear, kGateUp: a step's operands are read from LDS while the step before multiplies
+  uint4 fa[M == kDown ? 1 : MI], fb[2][M == kDown ? 1 : NJ];
+  if constexpr (M != kDown) {
+    wait_loads_barrier<(L::AHEAD - 1) * PER>();
+    const uint8_t* st = next_stage();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[i] = afrag(st, 0, i);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) fb[0][j] = bfrag(st, 0, j);
+  }
+#pragma unroll 1
   for (int cr = 0; cr < n_my; ++cr) {
-    const Item it = item_of(cr);
+    const Item it = cur;
     const int par = cr & 1;
+    // every wave is done with tile cr - 1: its lists and scales make room for tile cr + 1
+    lds_barrier();
+    aim(nxt, par ^ 1);
+    cur = nxt;
+    if (cr + 2 < n_my) nxt = item_of(cr + 2);
+    load_list(nxt, par);
     i32x4 acc[M == kDown ? 1 : MI][M == kDown ? 1 : NJ];
     f32x4 facc[M == kDown ? MI : 1][M == kDown ? NJ : 1];
     if constexpr (M == kDown) {
@@ -532,59 +568,66 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
         for (int j = 0; j < NJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     }
     const int blocks = (it.rows + 15) >> 4;                    // 16-row blocks with rows
-    const int nv = max(0, (blocks - wm + WM - 1) / WM);        // of them this wave's
-    auto loop = [&](auto nvc) {
-      constexpr int NV = decltype(nvc)::value;
-      for (int kt = 0; kt < nk; ++kt, ++gs) {
-        wait_stage<PER, L::STAGES - 2>(min(L::STAGES - 2, total - 1 - gs));
-        if (gs + L::STAGES - 1 < total) issue();               // every wave is past stage gs - 1
-        const uint8_t* st = lds + cslot * L::STAGE;
-        cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
-        auto bfrag = [&](int s, int j) {
-          const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2)
-                                     : wn * NJ + j;
-          return *reinterpret_cast<const uint4*>(st + L::SUB * L::A + s * L::B + b * 1024 + lane * 16);
-        };
-        auto afrag = [&](int s, int i) {
-          return *reinterpret_cast<const uint4*>(st + s * L::A + aoff + 16 * WM * i * kStep);
-        };
-        if constexpr (M == kDown) {
-          const bool two = 2 * kt + 1 < nsteps;
-          uint4 b0[NJ], b1[NJ];
+    const int nv = __builtin_amdgcn_readfirstlane(max(0, (blocks - wm + WM - 1) / WM));   // of them this wave's
+    if constexpr (M == kDown) {
+#pragma unroll 1
+      for (int kt = 0; kt < nk; ++kt) {
+        wait_loads_barrier<0>();                               // this stage is complete, every wave is past the last one
+        load_scales();
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            b0[j] = bfrag(0, j);
-            b1[j] = two ? bfrag(1, j) : make_uint4(0, 0, 0, 0);
-          }
-          const float* sc = reinterpret_cast<const float*>(st + L::SUB * (L::A + L::B));
+        for (int i = 0; i < PER; ++i) load(i);
+        loaded();
+        const uint8_t* st = next_stage();
+        const bool two = 2 * kt + 1 < nsteps;
+        const float* sc = reinterpret_cast<const float*>(st + L::SUB * (L::A + L::B));
+        uint4 a0[MI], a1[MI];
+        float s[MI];
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const uint4 a0 = afrag(0, i), a1 = afrag(1, i);
-            const int blk = wm + WM * i;
-            const float s = sc[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+        for (int i = 0; i < MI; ++i) {
+          a0[i] = afrag(st, 0, i);
+          a1[i] = two ? afrag(st, 1, i) : make_uint4(0, 0, 0, 0);
+          const int blk = wm + WM * i;
+          s[i] = sc[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+        }
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const i32x4 t = mfma_i8(b1[j], a1, mfma_i8(b0[j], a0, i32x4{0, 0, 0, 0}));
+        for (int j = 0; j < NJ; ++j) {
+          const uint4 b0 = bfrag(st, 0, j), b1 = bfrag(st, 1, j);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) facc[i][j][r] = __builtin_fmaf(static_cast<float>(t[r]), s, facc[i][j][r]);
-            }
-          }
-        } else {
-          uint4 b[NJ];
+          for (int i = 0; i < MI; ++i) {
+            const i32x4 t = mfma_i8(b1, a1[i], mfma_i8(b0, a0[i], i32x4{0, 0, 0, 0}));
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) b[j] = bfrag(0, j);
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const uint4 a = afrag(0, i);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_i8(b[j], a, acc[i][j]);
+            for (int r = 0; r < 4; ++r) facc[i][j][r] = __builtin_fmaf(static_cast<float>(t[r]), s[i], facc[i][j][r]);
           }
         }
       }
-    };
-    if (nv > MI / 2) loop(Int<MI>{});
-    else if (nv > MI / 4) loop(Int<MI / 2>{});
-    else loop(Int<MI / 4>{});
+    } else {
+      // One step on the operands fa, b (n: 16-row blocks to multiply); reads the next step's into
+      // fa (each block after its last use) and bn.
+      auto step = [&](int n, uint4 (&b)[NJ], uint4 (&bn)[NJ]) MOE_INLINE {
+        // the next stage is complete in LDS, and every wave is past the step before this one
+        wait_loads_barrier<(L::AHEAD - 2) * PER>();
+        const uint8_t* st = next_stage();
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+#pragma unroll
+          for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) bn[j] = bfrag(st, 0, j);
+#pragma unroll
+          for (int l = i * PER / MI; l < (i + 1) * PER / MI; ++l) load(l);
+          if (i < n) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_i8(b[j], fa[i], acc[i][j]);
+          }
+          fa[i] = afrag(st, 0, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        loaded();
+      };
+#pragma unroll 1
+      for (int kt = 0; kt < nk; kt += 2) {
+        step(nv, fb[0], fb[1]);
+        step(kt + 1 < nk ? nv : 0, fb[1], fb[0]);
+      }
+    }
 
     // ---- epilogue
     const float* sa = reinterpret_cast<const float*>(lds + L::SA + par * L::ROWS);
@@ -657,6 +700,8 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
       }
     }
   }
+  // the stages requested past the last tile land in LDS: not after this block has left it
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 int pick_mf(int avg) { return avg <= 12 ? 1 : avg <= 28 ? 2 : 4; }
@@ -671,7 +716,7 @@ int device_cus() {
 }
 
 #ifndef I8_CFG
-#define I8_CFG TileCfg<8, 8, 2, 2>
+#define I8_CFG TileCfg<4, 8, 4, 2>
 #endif
 using Tile = I8_CFG;
 constexpr int kTileMinAvg = 48;
