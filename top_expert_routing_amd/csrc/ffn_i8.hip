@@ -61,6 +61,46 @@ __device__ __forceinline__ i32x4 mfma_i8(const uint4& w, const uint4& x, const i
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), c, 0, 0, 0);
 }
 
+// Scale of a block of the SwiGLU product and the factor of its codes.  The products carry
+// errors of a few 2^-23 anyhow, so their codes are rounded from v * (1 / scale) without
+// the exact quotient's correction: a code moves only where the quotient lies within
+// 1e-4 of a border.
+struct BlockScale {
+  float scale, r;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+  const float s = __uint_as_float(amax_bits) * (1.0f / 127.0f);
+  if (amax_bits >= 0x7f800000u) return BlockScale{__builtin_nanf(""), 0.f};
+  if (s < 0x1p-126f) return BlockScale{1.f, 0.f};
+  return BlockScale{s, __builtin_amdgcn_rcpf(s)};
+}
+// Four codes: adding 1.5 * 2^23 rounds v * r to the nearest integer (halves to even) and
+// leaves its two's complement in the low bits; |v * r| <= 127.0001.
+__device__ __forceinline__ uint32_t block_codes(const float (&v)[4], float r) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__builtin_fmaf(v[i], r, 12582912.0f));
+  const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// Exchanges over the four 16-lane rows q of a wave, on gfx950's row swaps; every lane takes part.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {   // lanes 32-63 of a with lanes 0-31 of b
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0], b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {   // rows 1, 3 of a with rows 0, 2 of b
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0], b = r[1];
+}
+// d[j] of row q becomes d[q] of row j.
+__device__ __forceinline__ void transpose_rows(uint32_t (&d)[4]) {
+  swap32(d[0], d[2]);
+  swap32(d[1], d[3]);
+  swap16(d[0], d[1]);
+  swap16(d[2], d[3]);
+}
+
 // silu(g) * u; the hardware's exponential and reciprocal are within 2 ulp, far below
 // half a code of the quantisation that follows
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -262,11 +302,11 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_i8(ProductArgs p) {
       uint32_t big = amax[0][m];
 #pragma unroll
       for (int w = 1; w < kWavesS; ++w) big = max(big, amax[w][m]);
-      const QuantScale qs = quant_scale(big);
+      const BlockScale qs = block_scale(big);
       const int row = it.row(m);
       if (live)
         *reinterpret_cast<uint32_t*>(static_cast<int8_t*>(p.out) + static_cast<size_t>(row) * cols + n) =
-            pack_codes(quant_code(v[i][0], qs), quant_code(v[i][1], qs), quant_code(v[i][2], qs), quant_code(v[i][3], qs));
+            block_codes(v[i], qs.r);
       if (wave == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.scale;
     }
   } else {
@@ -304,8 +344,9 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_i8(ProductArgs p) {
 //     compiler sees would make it wait for everything in flight.
 // Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave,
 // so the rows of a partial tile spread over them.
-template <int MI_, int NJ_, int WM_, int WN_>
+template <int MI_, int NJ_, int WM_, int WN_, int BPC_>
 struct TileCfg {
+  static constexpr int BPC = BPC_;                             // blocks per CU
   static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = kWave * NW;
   static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
   static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;
@@ -315,18 +356,19 @@ struct TileCfg {
 template <class C, Mode M>
 struct TileLds {
   static constexpr int SUB = M == kDown ? 2 : 1;               // K steps per stage
-  static constexpr int STAGES = M == kDown ? 2 : 4;
-  static constexpr int AHEAD = M == kDown ? 1 : 3;             // stages requested before the first is used
+  static constexpr int STAGES = M == kDown ? 2 : C::BPC == 2 ? 3 : 4;
+  static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
   static constexpr int A = C::BM * kStep, B = C::BN * kStep;   // bytes per K step
-  static constexpr int ROWS = C::NW * kWave * 4;               // one 4-byte value per row slot
+  static constexpr int WROWS = 16 * C::ADMA * 4;               // one 4-byte value per row: of a wave's loads, of all
+  static constexpr int ROWS = C::NW * WROWS;
   static constexpr int STAGE = SUB * (A + B) + (M == kDown ? ROWS : 0);
   static constexpr int RING = STAGES * STAGE;
   static constexpr int LIST = RING;                            // row list of two tiles
   static constexpr int SA = LIST + 2 * ROWS;                   // row scales of two tiles
   static constexpr int SB = SA + 2 * ROWS;                     // channel scales of two tiles
   static constexpr int MAX = SB + 2 * 1024;                    // kGateUp: largest magnitudes
-  static constexpr int PLAN = MAX + C::WN * C::BM * 4;         // tiles before each group, group offsets
-  static int bytes(int G) { return PLAN + 8 * (G + 1); }
+  static constexpr int PLAN = MAX + C::WN * C::BM * 4;         // sums over waves, tiles before each group, group offsets
+  static int bytes(int G) { return PLAN + 4 * C::NW + 8 * (G + 1); }
 };
 
 __device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
@@ -370,16 +412,16 @@ __device__ __forceinline__ Item uniform(const Item& i) {
 }
 
 template <class C, Mode M, class Out>
-__global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
+__global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs p) {
   using L = TileLds<C, M>;
   constexpr int MI = C::MI, NJ = C::NJ, WM = C::WM, WN = C::WN, NW = C::NW, NT = C::NT, BM = C::BM;
   constexpr int OUTC = M == kGateUp ? C::BN / 2 : C::BN;
   constexpr int GPT = (kMaxGroups + NT - 1) / NT;
   constexpr int kPanel = 4;                                    // column chunks that follow each other per m-tile
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  int* before = reinterpret_cast<int*>(lds + L::PLAN);         // m-tiles before group g
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  int* wsum = reinterpret_cast<int*>(lds + L::PLAN);
+  int* before = wsum + NW;                                     // m-tiles before group g
   int* offs = before + p.G + 1;
-  __shared__ int wsum[NW];
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
   const int K = p.K, cols = p.cols;
@@ -445,14 +487,17 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
   uint32_t ao[C::ADMA], ao_next[C::ADMA];                      // this lane's bytes from p.a: tile being loaded, tile after it
   const int8_t *bp[C::BDMA], *bp_next[C::BDMA];                // wave-uniform
   const float *sp = nullptr, *sp_next = nullptr;               // kDown: this lane's row's block scales
-  // this lane's row in 4-byte loads of one value per row: slots of wave w are [64 w, 64 w + 64)
-  const int vrow = 16 * (wave + NW * min(lane >> 4, C::ADMA - 1)) + l16;
+  // 4-byte loads of one value per row: lane 16 i + r of a wave has row r of the 16 rows of its
+  // load i, so wave w's values are the w-th 16 * ADMA of ROWS
+  const bool vlane = lane < 16 * C::ADMA;
+  const int vrow = 16 * (wave + NW * (lane >> 4)) + l16;
   auto load_list = [&](const Item& it, int parity) MOE_INLINE {
-    if (p.x_rows) dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * 256);
+    if (p.x_rows && vlane)
+      dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * L::WROWS);
   };
   // Sources of a tile whose row list has arrived; requests its scales.
   auto aim = [&](const Item& it, int parity) MOE_INLINE {
-    const int* list = reinterpret_cast<const int*>(lds + L::LIST + parity * L::ROWS) + wave * 64;
+    const int* list = reinterpret_cast<const int*>(lds + L::LIST + parity * L::ROWS + wave * L::WROWS);
     auto src = [&](int r, int slot) MOE_INLINE {
       return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : it.row(min(r, it.rows - 1));
     };
@@ -476,7 +521,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
       dma16((up ? p.s1 : p.s0) + e0 + n, lds0 + L::SB + parity * 1024);
     }
     if constexpr (M == kDown) sp_next = p.as + it.row(min(vrow, it.rows - 1));
-    else dma4(p.as + src(vrow, min(lane, 16 * C::ADMA - 1)), lds0 + L::SA + parity * L::ROWS + wave * 256);
+    else if (vlane) dma4(p.as + src(vrow, lane), lds0 + L::SA + parity * L::ROWS + wave * L::WROWS);
   };
   int ikt = 0, islot = 0;                                      // the stage requested next: of its tile, ring slot
   auto turn = [&]() MOE_INLINE {                               // go on with the next tile
@@ -503,7 +548,8 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
   };
   auto load_scales = [&]() MOE_INLINE {
     if constexpr (M == kDown)
-      dma4(sp + static_cast<size_t>(ikt) * p.n_rows, lds0 + islot * L::STAGE + L::SUB * (L::A + L::B) + wave * 256);
+      if (vlane)
+        dma4(sp + static_cast<size_t>(ikt) * p.n_rows, lds0 + islot * L::STAGE + L::SUB * (L::A + L::B) + wave * L::WROWS);
   };
   Item cur = item_of(0), nxt = n_my > 1 ? item_of(1) : cur;
   load_list(cur, 0);
@@ -587,17 +633,38 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
           a0[i] = afrag(st, 0, i);
           a1[i] = two ? afrag(st, 1, i) : make_uint4(0, 0, 0, 0);
           const int blk = wm + WM * i;
-          s[i] = sc[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+          s[i] = sc[(blk % NW) * (16 * C::ADMA) + (blk / NW) * 16 + l16];
         }
+        // the sums of column block j are scaled into facc while block j + 1 multiplies
+        uint4 b0 = bfrag(st, 0, 0), b1 = bfrag(st, 1, 0);
+        i32x4 t[2][MI];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const uint4 b0 = bfrag(st, 0, j), b1 = bfrag(st, 1, j);
+        for (int j = 0; j <= NJ; ++j) {
+          uint4 c0, c1;
+          if (j + 1 < NJ) c0 = bfrag(st, 0, j + 1), c1 = bfrag(st, 1, j + 1);
+          if (j < NJ) {
 #pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            const i32x4 t = mfma_i8(b1, a1[i], mfma_i8(b0, a0[i], i32x4{0, 0, 0, 0}));
+            for (int i = 0; i < MI; ++i) t[j & 1][i] = mfma_i8(b0, a0[i], i32x4{0, 0, 0, 0});
 #pragma unroll
-            for (int r = 0; r < 4; ++r) facc[i][j][r] = __builtin_fmaf(static_cast<float>(t[r]), s[i], facc[i][j][r]);
+            for (int i = 0; i < MI; ++i) t[j & 1][i] = mfma_i8(b1, a1[i], t[j & 1][i]);
           }
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                facc[i][j - 1][r] = __builtin_fmaf(static_cast<float>(t[(j - 1) & 1][i][r]), s[i], facc[i][j - 1][r]);
+          }
+          if (j > 0 && j < NJ) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // the reads first, then one product, four
+#pragma unroll
+            for (int i = 0; i < 2 * MI; ++i) {                   // conversions or sums, one product, ...
+              __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          b0 = c0, b1 = c1;
         }
       }
     } else {
@@ -639,7 +706,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int blk = wm + WM * i;
-        const float sx = sa[(blk % NW) * 64 + (blk / NW) * 16 + l16];
+        const float sx = sa[(blk % NW) * (16 * C::ADMA) + (blk / NW) * 16 + l16];
         uint32_t big = 0;
 #pragma unroll
         for (int j = 0; j < NJ / 2; ++j) {
@@ -660,42 +727,63 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_i8(ProductArgs p) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = 16 * (wm + WM * i) + l16;
-        if (m >= it.rows) continue;
+        if (16 * (wm + WM * i) >= it.rows) continue;           // wave-uniform; the exchange below needs every lane
         uint32_t big = mx[m];
 #pragma unroll
         for (int w = 1; w < WN; ++w) big = max(big, mx[w * BM + m]);
-        const QuantScale qs = quant_scale(big);
-        const int row = it.row(m);
-        if (wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.scale;
+        const BlockScale qs = block_scale(big);
+        static_assert(NJ / 2 == 4, "one 16-byte store per row and lane");
+        uint32_t d[4];
 #pragma unroll
-        for (int j = 0; j < NJ / 2; ++j) {
-          const int n = n0 + 16 * (wn * (NJ / 2) + j) + 4 * q;
-          if (n < cols)
-            *reinterpret_cast<uint32_t*>(static_cast<int8_t*>(p.out) + static_cast<size_t>(row) * cols + n) =
-                pack_codes(quant_code(v[i][j][0], qs), quant_code(v[i][j][1], qs), quant_code(v[i][j][2], qs),
-                           quant_code(v[i][j][3], qs));
-        }
+        for (int j = 0; j < 4; ++j) d[j] = block_codes(v[i][j], qs.r);
+        transpose_rows(d);                                     // now lane 16 q + r: the 16 columns of block q
+        if (m >= it.rows) continue;
+        const int row = it.row(m), n = n0 + 16 * (wn * 4 + q);
+        if (wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.scale;
+        if (n < cols)
+          *reinterpret_cast<uint4*>(static_cast<int8_t*>(p.out) + static_cast<size_t>(row) * cols + n) =
+              make_uint4(d[0], d[1], d[2], d[3]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int blk = wm + WM * i, m = 16 * blk + l16;
-        if (m >= it.rows) continue;
+        if (16 * blk >= it.rows) continue;                     // wave-uniform
         float sx = 1.f;
-        if constexpr (M == kLinear) sx = sa[(blk % NW) * 64 + (blk / NW) * 16 + l16];
-        Out* orow = static_cast<Out*>(p.out) + static_cast<size_t>(it.row(m)) * cols;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int c = 16 * (wn * NJ + j) + 4 * q;
-          if (n0 + c >= cols) continue;
-          const f32x4 w0 = *reinterpret_cast<const f32x4*>(sb + c);
-          float v[4];
+        if constexpr (M == kLinear) sx = sa[(blk % NW) * (16 * C::ADMA) + (blk / NW) * 16 + l16];
+        const bool in = m < it.rows;
+        Out* orow = static_cast<Out*>(p.out) + static_cast<size_t>(it.row(in ? m : 0)) * cols + n0;
+        auto values = [&](int j, float (&v)[4]) MOE_INLINE {
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(sb + 16 * (wn * NJ + j) + 4 * q);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if constexpr (M == kDown) v[r] = facc[i][j][r] * w0[r];
             else v[r] = static_cast<float>(acc[i][j][r]) * (sx * w0[r]);
           }
-          store4(orow + n0 + c, v);
+        };
+        if constexpr (sizeof(Out) == 4) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            float v[4];
+            values(j, v);
+            const int c = 16 * (wn * NJ + j) + 4 * q;
+            if (in && n0 + c < cols) store4(orow + c, v);
+          }
+        } else {
+          // bf16: two column blocks to 16 bytes a lane: row q = 2 a + b gets columns 8 b .. 8 b + 7 of block j + a
+#pragma unroll
+          for (int j = 0; j < NJ; j += 2) {
+            float v[4], u[4];
+            values(j, v);
+            values(j + 1, u);
+            uint32_t d[4] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
+            swap32(d[0], d[2]);
+            swap32(d[1], d[3]);
+            swap16(d[0], d[2]);
+            swap16(d[1], d[3]);
+            const int c = 16 * (wn * NJ + j + (q >> 1)) + 8 * (q & 1);
+            if (in && n0 + c < cols) *reinterpret_cast<uint4*>(orow + c) = make_uint4(d[0], d[1], d[2], d[3]);
+          }
         }
       }
     }
@@ -715,20 +803,26 @@ int device_cus() {
   return cus;
 }
 
-#ifndef I8_CFG
-#define I8_CFG TileCfg<4, 8, 4, 2>
-#endif
-using Tile = I8_CFG;
+using TileWide = TileCfg<4, 8, 4, 2, 1>;   // 256 rows, one block of eight waves per CU
+using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves per CU
 constexpr int kTileMinAvg = 48;
+constexpr int kLdsPerCu = 160 * 1024;
 constexpr int kTileMinK = 4 * kStep;   // the row list of a tile is loaded a tile ahead: at least STAGES - 1 steps
 
 template <Mode M, class Out>
 void launch_product(const ProductArgs& p, hipStream_t stream) {
   const int avg = p.n_rows / p.G;
   if (avg > kTileMinAvg && p.K >= kTileMinK) {
-    const int grid = (device_cus() + kXcds - 1) / kXcds * kXcds;
-    const size_t lds = TileLds<Tile, M>::bytes(p.G);
-    hipLaunchKernelGGL((tile_i8<Tile, M, Out>), dim3(grid), dim3(Tile::NT), lds, stream, p);
+    const int cus = (device_cus() + kXcds - 1) / kXcds * kXcds;
+    if constexpr (M != kDown) {
+      const size_t lds = TileLds<TileHalf, M>::bytes(p.G);
+      if (lds <= kLdsPerCu / 2) {
+        hipLaunchKernelGGL((tile_i8<TileHalf, M, Out>), dim3(2 * cus), dim3(TileHalf::NT), lds, stream, p);
+        return;
+      }
+    }
+    const size_t lds = TileLds<TileWide, M>::bytes(p.G);
+    hipLaunchKernelGGL((tile_i8<TileWide, M, Out>), dim3(cus), dim3(TileWide::NT), lds, stream, p);
     return;
   }
   const int mf = pick_mf(avg);
