@@ -57,6 +57,23 @@ def _same_device(first: torch.Tensor, **others: Optional[torch.Tensor]):
             raise ValueError(f"{name} must be on {first.device}, got {t.device}")
 
 
+def _ok(t: torch.Tensor, index: int, dtype, shape) -> bool:
+    """A contiguous tensor of this dtype and shape on GPU `index` (the checks of
+    _out and _same_device in one cheap test: a small call's time is its host side)."""
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+
+
+def _call(name: str, index: int, fn, *args) -> None:
+    """fn(*args, stream) on GPU `index` and its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != _lib.MOE_OK:
+        raise _lib.MoeError(name, status)
+
+
 def _workspace(fn, args_before_ws, dev) -> torch.Tensor:
     """Query a call's workspace size (NULL workspace) and allocate it."""
     n = ctypes.c_size_t(0)
@@ -135,26 +152,25 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[t
     best stay (all, if not given), weights renormalised and scaled."""
     _need(logits, "logits", None, 2)
     T, E = logits.shape
-    dev = logits.device
+    index = logits.get_device()
     if score not in _lib.SCORES:
         raise ValueError(f"score must be one of {sorted(_lib.SCORES)}")
     if group_rank not in _lib.GROUP_RANKS:
         raise ValueError(f"group_rank must be one of {sorted(_lib.GROUP_RANKS)}")
-    if bias is not None:
-        _out(bias, "bias", torch.float32, (E,))
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _out(topk_ids, "topk_ids", torch.int32, (T, k))
-    _out(topk_w, "topk_w", torch.float32, (T, k))
-    _same_device(logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        check("moe_route", lib.moe_route(
-            _ptr(logits), _dtype_code(logits), _ptr(bias), T, E, k, _lib.SCORES[score], n_groups,
-            n_groups if top_groups is None else top_groups, _lib.GROUP_RANKS[group_rank], int(bool(renormalize)),
-            float(scale), _ptr(topk_ids), _ptr(topk_w), _stream(dev)))
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    if not ((bias is None or _ok(bias, index, torch.float32, (E,))) and _ok(topk_ids, index, torch.int32, (T, k)) and
+            _ok(topk_w, index, torch.float32, (T, k))):
+        if bias is not None:
+            _out(bias, "bias", torch.float32, (E,))
+        _out(topk_ids, "topk_ids", torch.int32, (T, k))
+        _out(topk_w, "topk_w", torch.float32, (T, k))
+        _same_device(logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
+    _call("moe_route", index, _lib.load().moe_route, logits.data_ptr(), _dtype_code(logits), _ptr(bias), T, E, k,
+          _lib.SCORES[score], n_groups, n_groups if top_groups is None else top_groups, _lib.GROUP_RANKS[group_rank],
+          1 if renormalize else 0, scale, topk_ids.data_ptr(), topk_w.data_ptr())
     return topk_ids, topk_w
 
 
@@ -526,13 +542,13 @@ def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optio
         q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     if s is None:
         s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _out(q, "q", torch.int8, x.shape)
-    _out(s, "s", torch.float32, x.shape[:-1])
-    _same_device(x, q=q, s=s)
-    lib = _lib.load()
-    with torch.cuda.device(x.device):
-        check("moe_quantize_rows_i8", lib.moe_quantize_rows_i8(_ptr(x), _dtype_code(x), s.numel(), x.shape[-1],
-                                                               _ptr(q), _ptr(s), _stream(x.device)))
+    index = x.get_device()
+    if not (_ok(q, index, torch.int8, x.shape) and _ok(s, index, torch.float32, x.shape[:-1])):
+        _out(q, "q", torch.int8, x.shape)
+        _out(s, "s", torch.float32, x.shape[:-1])
+        _same_device(x, q=q, s=s)
+    _call("moe_quantize_rows_i8", index, _lib.load().moe_quantize_rows_i8, x.data_ptr(), _dtype_code(x), s.numel(),
+          x.shape[-1], q.data_ptr(), s.data_ptr())
     return q, s
 
 
@@ -544,14 +560,19 @@ def pack_i8_codes(q: torch.Tensor) -> torch.Tensor:
     return pack_fp8_codes(q)
 
 
-def _i8_batch(x_rows, group_offsets, E, n_shared, nseg, n_x):
+def _i8_batch(x, x_rows, group_offsets, E, n_shared, nseg):
     """Checks of a grouped int8 call's row list and offsets; its sorted rows."""
-    _need(group_offsets, "group_offsets", torch.int32, 1)
-    if group_offsets.numel() != nseg * E + n_shared + 1:
-        raise ValueError("group_offsets must have nseg*E + n_shared + 1 entries")
+    index, entries = x.get_device(), nseg * E + n_shared + 1
+    if not _ok(group_offsets, index, torch.int32, (entries,)):
+        _need(group_offsets, "group_offsets", torch.int32, 1)
+        if group_offsets.numel() != entries:
+            raise ValueError("group_offsets must have nseg*E + n_shared + 1 entries")
+        _same_device(x, group_offsets=group_offsets)
     if x_rows is None:
-        return n_x
-    _need(x_rows, "x_rows", torch.int32, 1)
+        return x.shape[0]
+    if not _ok(x_rows, index, torch.int32, (x_rows.numel(),)):
+        _need(x_rows, "x_rows", torch.int32, 1)
+        _same_device(x, x_rows=x_rows)
     return x_rows.numel()
 
 
@@ -563,23 +584,23 @@ def grouped_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, group_offsets: to
     out (y's dtype, or `out_dtype`).  E = 1 with offsets [0, N] is a plain
     linear map (moe_grouped_linear_i8)."""
     _need(xq, "xq", torch.int8, 2)
-    n_x, K = xq.shape
-    _out(x_scale, "x_scale", torch.float32, (n_x,))
     _need(w, "w", torch.int8, 3)
-    N = _i8_batch(x_rows, group_offsets, E, n_shared, nseg, n_x)
-    O = w.shape[1]
-    if w.shape != (E + n_shared, O, K):
-        raise ValueError("w must be [E+S][O][K]")
-    _out(w_scale, "w_scale", torch.float32, (E + n_shared, O))
+    n_x, K = xq.shape
+    G, O = E + n_shared, w.shape[1]
+    index = xq.get_device()
+    N = _i8_batch(xq, x_rows, group_offsets, E, n_shared, nseg)
     if y is None:
         y = torch.empty((N, O), dtype=out_dtype, device=xq.device)
-    _out(y, "y", y.dtype, (N, O))
-    _same_device(xq, x_scale=x_scale, group_offsets=group_offsets, w=w, w_scale=w_scale, y=y, x_rows=x_rows)
-    lib = _lib.load()
-    with torch.cuda.device(xq.device):
-        check("moe_grouped_linear_i8", lib.moe_grouped_linear_i8(
-            _ptr(xq), _ptr(x_scale), _ptr(x_rows), n_x, _ptr(group_offsets), N, E, n_shared, nseg, K, O, _ptr(w),
-            _ptr(w_scale), _dtype_code(y), _ptr(y), _stream(xq.device)))
+    if not (_ok(x_scale, index, torch.float32, (n_x,)) and _ok(w, index, torch.int8, (G, O, K)) and
+            _ok(w_scale, index, torch.float32, (G, O)) and _ok(y, index, y.dtype, (N, O))):
+        _out(x_scale, "x_scale", torch.float32, (n_x,))
+        _out(w, "w", torch.int8, (G, O, K))
+        _out(w_scale, "w_scale", torch.float32, (G, O))
+        _out(y, "y", y.dtype, (N, O))
+        _same_device(xq, x_scale=x_scale, w=w, w_scale=w_scale, y=y)
+    _call("moe_grouped_linear_i8", index, _lib.load().moe_grouped_linear_i8, xq.data_ptr(), x_scale.data_ptr(),
+          _ptr(x_rows), n_x, group_offsets.data_ptr(), N, E, n_shared, nseg, K, O, w.data_ptr(), w_scale.data_ptr(),
+          _dtype_code(y), y.data_ptr())
     return y
 
 
@@ -602,33 +623,29 @@ def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_share
     scales and int8 activations; bf16 token rows, read directly or through
     `x_rows`, bf16 out (moe_grouped_ffn_i8)."""
     _need(x, "x", torch.bfloat16, 2)
-    for t, n in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
-        _need(t, n, torch.int8, 3)
+    _need(w_gate, "w_gate", torch.int8, 3)
     n_x, d = x.shape
-    N = _i8_batch(x_rows, group_offsets, E, n_shared, nseg, n_x)
-    I = w_gate.shape[1]
-    G = E + n_shared
-    if w_gate.shape != (G, I, d) or w_up.shape != w_gate.shape or w_down.shape != (G, d, I):
-        raise ValueError("expert weight codes must be [E+S][I][d] (gate, up) and [E+S][d][I] (down)")
-    for t, n, width in ((s_gate, "s_gate", I), (s_up, "s_up", I), (s_down, "s_down", d)):
-        _out(t, n, torch.float32, (G, width))
-    dev = x.device
+    I, G = w_gate.shape[1], E + n_shared
+    index = x.get_device()
+    N = _i8_batch(x, x_rows, group_offsets, E, n_shared, nseg)
     if h_sorted is None:
-        h_sorted = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
-    _out(h_sorted, "h_sorted", torch.bfloat16, (N, d))
+        h_sorted = torch.empty((N, d), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = torch.empty(max(ffn_i8_workspace_bytes(N, n_x, d, I, E, n_shared, nseg), 256), dtype=torch.uint8,
-                                device=dev)
-    _need(workspace, "workspace", torch.uint8, 1)
-    _same_device(x, group_offsets=group_offsets, w_gate=w_gate, s_gate=s_gate, w_up=w_up, s_up=s_up, w_down=w_down,
-                 s_down=s_down, h_sorted=h_sorted, workspace=workspace, x_rows=x_rows)
-    lib = _lib.load()
+                                device=x.device)
+    need = (("w_gate", w_gate, torch.int8, (G, I, d)), ("s_gate", s_gate, torch.float32, (G, I)),
+            ("w_up", w_up, torch.int8, (G, I, d)), ("s_up", s_up, torch.float32, (G, I)),
+            ("w_down", w_down, torch.int8, (G, d, I)), ("s_down", s_down, torch.float32, (G, d)),
+            ("h_sorted", h_sorted, torch.bfloat16, (N, d)), ("workspace", workspace, torch.uint8, (workspace.numel(),)))
+    for name, t, dtype, shape in need:
+        if not _ok(t, index, dtype, shape):
+            _out(t, name, dtype, shape)
+            _same_device(x, **{name: t})
     nbytes = ctypes.c_size_t(workspace.numel())
-    with torch.cuda.device(dev):
-        check("moe_grouped_ffn_i8", lib.moe_grouped_ffn_i8(
-            _ptr(x), _ptr(x_rows), n_x, _ptr(group_offsets), N, E, n_shared, nseg, d, I, _ptr(w_gate), _ptr(s_gate),
-            _ptr(w_up), _ptr(s_up), _ptr(w_down), _ptr(s_down), _ptr(h_sorted), _ptr(workspace), ctypes.byref(nbytes),
-            _stream(dev)))
+    _call("moe_grouped_ffn_i8", index, _lib.load().moe_grouped_ffn_i8, x.data_ptr(), _ptr(x_rows), n_x,
+          group_offsets.data_ptr(), N, E, n_shared, nseg, d, I, w_gate.data_ptr(), s_gate.data_ptr(), w_up.data_ptr(),
+          s_up.data_ptr(), w_down.data_ptr(), s_down.data_ptr(), h_sorted.data_ptr(), workspace.data_ptr(),
+          ctypes.byref(nbytes))
     return h_sorted
 
 

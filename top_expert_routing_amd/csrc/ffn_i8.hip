@@ -80,8 +80,7 @@ __device__ __forceinline__ uint32_t block_codes(const float (&v)[4], float r) {
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__builtin_fmaf(v[i], r, 12582912.0f));
-  const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400u);
-  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+  return low_bytes(c[0], c[1], c[2], c[3]);
 }
 
 // Exchanges over the four 16-lane rows q of a wave, on gfx950's row swaps; every lane takes part.
@@ -350,18 +349,20 @@ struct TileCfg {
   static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = kWave * NW;
   static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
   static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;
-  static_assert(BN == 2 * kBlock, "a tile holds the columns of one scale");
   static_assert(ADMA >= 1 && ADMA <= 4 && BDMA >= 1, "DMA instructions per wave");
 };
+constexpr int kLdsPerCu = 160 * 1024;
 template <class C, Mode M>
 struct TileLds {
   static constexpr int SUB = M == kDown ? 2 : 1;               // K steps per stage
-  static constexpr int STAGES = M == kDown ? 2 : C::BPC == 2 ? 3 : 4;
-  static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
   static constexpr int A = C::BM * kStep, B = C::BN * kStep;   // bytes per K step
   static constexpr int WROWS = 16 * C::ADMA * 4;               // one 4-byte value per row: of a wave's loads, of all
   static constexpr int ROWS = C::NW * WROWS;
   static constexpr int STAGE = SUB * (A + B) + (M == kDown ? ROWS : 0);
+  // as many as fit beside 12 KiB (two blocks per CU: 8) of lists, scales and the plan
+  static constexpr int STAGES = (kLdsPerCu / C::BPC - (C::BPC == 2 ? 8 : 12) * 1024) / STAGE;
+  static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
+  static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
   static constexpr int RING = STAGES * STAGE;
   static constexpr int LIST = RING;                            // row list of two tiles
   static constexpr int SA = LIST + 2 * ROWS;                   // row scales of two tiles
@@ -618,7 +619,7 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
     if constexpr (M == kDown) {
 #pragma unroll 1
       for (int kt = 0; kt < nk; ++kt) {
-        wait_loads_barrier<0>();                               // this stage is complete, every wave is past the last one
+        wait_loads_barrier<(L::AHEAD - 1) * PER>();            // this stage is complete, every wave is past the last one
         load_scales();
 #pragma unroll
         for (int i = 0; i < PER; ++i) load(i);
@@ -635,13 +636,14 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
           const int blk = wm + WM * i;
           s[i] = sc[(blk % NW) * (16 * C::ADMA) + (blk / NW) * 16 + l16];
         }
-        // the sums of column block j are scaled into facc while block j + 1 multiplies
-        uint4 b0 = bfrag(st, 0, 0), b1 = bfrag(st, 1, 0);
+        // the sums of column block j are scaled into facc while block j + 1 multiplies,
+        // and the operands of block j + 2 are read
+        uint4 b0 = bfrag(st, 0, 0), b1 = bfrag(st, 1, 0), d0 = bfrag(st, 0, 1), d1 = bfrag(st, 1, 1);
         i32x4 t[2][MI];
 #pragma unroll
         for (int j = 0; j <= NJ; ++j) {
           uint4 c0, c1;
-          if (j + 1 < NJ) c0 = bfrag(st, 0, j + 1), c1 = bfrag(st, 1, j + 1);
+          if (j + 2 < NJ) c0 = bfrag(st, 0, j + 2), c1 = bfrag(st, 1, j + 2);
           if (j < NJ) {
 #pragma unroll
             for (int i = 0; i < MI; ++i) t[j & 1][i] = mfma_i8(b0, a0[i], i32x4{0, 0, 0, 0});
@@ -664,7 +666,7 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
             }
           }
           __builtin_amdgcn_sched_barrier(0);
-          b0 = c0, b1 = c1;
+          b0 = d0, b1 = d1, d0 = c0, d1 = c1;
         }
       }
     } else {
@@ -804,9 +806,9 @@ int device_cus() {
 }
 
 using TileWide = TileCfg<4, 8, 4, 2, 1>;   // 256 rows, one block of eight waves per CU
+using TileDown = TileCfg<4, 8, 4, 2, 1>;
 using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves per CU
 constexpr int kTileMinAvg = 48;
-constexpr int kLdsPerCu = 160 * 1024;
 constexpr int kTileMinK = 4 * kStep;   // the row list of a tile is loaded a tile ahead: at least STAGES - 1 steps
 
 template <Mode M, class Out>
@@ -821,8 +823,9 @@ void launch_product(const ProductArgs& p, hipStream_t stream) {
         return;
       }
     }
-    const size_t lds = TileLds<TileWide, M>::bytes(p.G);
-    hipLaunchKernelGGL((tile_i8<TileWide, M, Out>), dim3(cus), dim3(TileWide::NT), lds, stream, p);
+    using Tile = std::conditional_t<M == kDown, TileDown, TileWide>;
+    const size_t lds = TileLds<Tile, M>::bytes(p.G);
+    hipLaunchKernelGGL((tile_i8<Tile, M, Out>), dim3(cus * Tile::BPC), dim3(Tile::NT), lds, stream, p);
     return;
   }
   const int mf = pick_mf(avg);

@@ -21,6 +21,7 @@ struct RouteArgs {
   int bf16;      // logits: 1 bf16, 0 fp32
   int sigmoid;   // 0: softmax
   int n_groups, top_groups;
+  int group_lanes = 0;   // set by the launcher: lanes that hold a group's experts (0: no whole, power-of-two run)
   int top2;      // group value: sum of the two best, 0: the best
   int renormalize;
   float scale;

@@ -49,4 +49,33 @@ __device__ __forceinline__ uint32_t pack_codes(int a, int b, int c, int d) {
   return (a & 0xff) | ((b & 0xff) << 8) | ((c & 0xff) << 16) | (static_cast<uint32_t>(d) << 24);
 }
 
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// The codes of eight values of one row (its scale the same for the whole wavefront).
+// Adding 1.5 * 2^23 to v * r rounds it to the nearest integer c and leaves c's two's
+// complement in the low bits.  c is right if the remainder stays below half a step;
+// where some lane's does not (next to a border, 1 of 10^5 values), or the scale is
+// not an ordinary one, the wavefront takes quant_code.
+__device__ __forceinline__ uint2 quant_codes8(const float (&v)[8], const QuantScale& q) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t c[8];
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float m = __builtin_fmaf(v[j], q.r, kMagic);
+    c[j] = __float_as_uint(m);
+    far = fmaxf(far, fabsf(__builtin_fmaf(kMagic - m, q.s, v[j])));
+  }
+  const bool plain = q.up == 1.0f && q.r != 0.0f && far < 0.5f * q.s;
+  if (__all(plain)) return make_uint2(low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7]));
+  int e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) e[j] = quant_code(v[j], q);
+  return make_uint2(pack_codes(e[0], e[1], e[2], e[3]), pack_codes(e[4], e[5], e[6], e[7]));
+}
+
 }  // namespace moe
