@@ -41,6 +41,8 @@ constexpr int kStep = 64;            // K of one matrix instruction
 constexpr int kMaxGroups = 2 * 512 + 256;
 
 struct ProductArgs {
+  const void* x;           // few_i8<kGateUp>: bf16 tokens [n_x][K], in place of a and as
+  const float* af;         // few_i8<kDown>: the SwiGLU product [n_rows][K], in place of a and as
   const int8_t* a;         // codes of the rows: [n_x][K]; kDown: [n_rows][K]
   const float* as;         // their scales: [n_x]; kDown: [ceil(K / 128)][n_rows]
   const int8_t *w0, *w1;   // packed matrices [E+S][cols][K] (w1: up rows of kGateUp)
@@ -170,7 +172,7 @@ __device__ Item find_item(const ProductArgs& p, int BM, int nch) {
 }
 
 template <int MF, Mode M, class Out>
-__global__ __launch_bounds__(kThreadsS, 4) void stream_i8(ProductArgs p) {
+__global__ __launch_bounds__(kThreadsS, MF == 4 ? 2 : 4) void stream_i8(ProductArgs p) {
   constexpr int BM = 16 * MF;
   constexpr int NF = M == kGateUp ? 2 : 1;
   constexpr int U = kChunk / kStep;
@@ -327,6 +329,187 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_i8(ProductArgs p) {
       store4(static_cast<Out*>(p.out) + static_cast<size_t>(row) * cols + n, v);
     }
   }
+}
+
+// ---- few rows: 16 columns per block, K split over its waves --------------------------
+// With few rows (one token's experts, a small dense batch) 128-column items are too few
+// to draw the weights through every CU, so an item is 16 columns (kGateUp: 16 gate and 16
+// up rows) of at most 16 rows and the eight waves split K; their sums are joined through
+// LDS.  A wave's first weights are requested before anything else happens.
+// The FFN's quantisations move to where codes are used, because a block no longer holds
+// the columns that share a scale, and each block repeats them (16 rows at most):
+//   * kGateUp reads the bf16 tokens: a wave's slice of K gives part of a row's largest
+//     magnitude, LDS the rest; then the slice's codes are made next to the weights' loads.
+//     This saves the launch that quantises the tokens.
+//   * it writes the SwiGLU product in fp32 (N * I * 4 bytes, at most 80 KiB here), and
+//     kDown's waves, each on whole blocks of 128 columns, quantise it as they read it.
+constexpr int kFewSteps = 4;            // K steps in flight per wave
+constexpr int kSplit = kWavesS;
+
+// Codes of the eight values of row piece v, as quant_codes8, per-lane scales.
+__device__ __forceinline__ uint4 bf16_codes(const uint4& lo, const uint4& hi, const QuantScale& qs) {
+  auto eight = [&](const uint4& u) MOE_INLINE {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return quant_codes8(v, qs);
+  };
+  const uint2 a = eight(lo), b = eight(hi);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ uint32_t bf16_max(const uint4& u) {      // largest magnitude's fp32 bits
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+  return m;
+}
+__device__ __forceinline__ uint32_t max_over_q(uint32_t m) {        // over the four lanes of a row
+  m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16, kWave)));
+  return max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32, kWave)));
+}
+
+template <int NC, Mode M, class Out>
+__global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs p) {
+  constexpr int NF = M == kGateUp ? 2 * NC : NC, U = kFewSteps;   // j < NC: gate or only, j >= NC: up
+  __shared__ i32x4 part[kSplit][NF][kWave];
+  __shared__ uint32_t amax[kSplit][16];
+  const Item it = find_item(p, 16, p.cols / (16 * NC));
+  if (it.rows == 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+  const int l16 = lane & 15, q = lane >> 4;
+  const int K = p.K, cols = p.cols;
+  // this wave's K: whole blocks of 128, dealt in equal runs
+  const int run = ((K + kBlock - 1) / kBlock + kSplit - 1) / kSplit * kBlock;
+  const int k0 = min(K, wave * run), k1 = min(K, k0 + run);
+  const size_t rb = static_cast<size_t>(it.expert) * cols + it.chunk * 16 * NC;
+  const int8_t* wp[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) wp[j] = (j < NC ? p.w0 : p.w1) + (rb + 16 * (j % NC)) * K + lane * 16;
+  uint4 w[U][NF];
+  auto load_w = [&](int k) MOE_INLINE {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        w[u][j] = k + u * kStep < k1 ? *reinterpret_cast<const uint4*>(wp[j] + static_cast<size_t>(k + u * kStep) * 16)
+                                     : make_uint4(0, 0, 0, 0);
+  };
+  load_w(k0);
+  const int row = it.row(min(l16, it.rows - 1));            // lanes past the rows repeat the last one
+  const int src = M == kDown ? row : src_row(p, row);
+
+  QuantScale qs{1.f, 1.f, 1.f, 1.f};                        // kGateUp: of this lane's token
+  const uint16_t* xr = nullptr;
+  if constexpr (M == kGateUp) {
+    xr = static_cast<const uint16_t*>(p.x) + static_cast<size_t>(src) * K + 16 * q;
+    uint32_t m = 0;
+    for (int k = k0; k < k1; k += kStep) {
+      const uint4* v = reinterpret_cast<const uint4*>(xr + k);
+      m = max(m, max(bf16_max(v[0]), bf16_max(v[1])));
+    }
+    m = max_over_q(m);
+    if (q == 0) amax[wave][l16] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSplit; ++i) m = max(m, amax[i][l16]);
+    qs = quant_scale(m);
+  }
+  i32x4 acc[NF];
+  f32x4 facc[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) facc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NF; ++j) acc[j] = i32x4{0, 0, 0, 0};
+  for (int k = k0; k < k1; k += U * kStep) {
+    if (k != k0) load_w(k);
+    if constexpr (M == kDown) {
+      // blocks of 128 columns of the fp32 product: their scale, then their codes
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {
+        const int kb = k + u * kStep;
+        if (kb >= k1) break;
+        const bool two = kb + kStep < k1;
+        const float* ar = p.af + static_cast<size_t>(row) * K + kb + 16 * q;
+        float v[8][4];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const f32x4 f = i < 4 || two ? *reinterpret_cast<const f32x4*>(ar + (i / 4) * kStep + 4 * (i % 4)) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v[i][r] = f[r];
+            m = max(m, abs_bits(f[r]));
+          }
+        }
+        const BlockScale bs = block_scale(max_over_q(m));
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = block_codes(v[i], bs.r);
+        const uint4 a0 = make_uint4(c[0], c[1], c[2], c[3]), a1 = make_uint4(c[4], c[5], c[6], c[7]);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const i32x4 t = mfma_i8(w[u + 1][j], a1, mfma_i8(w[u][j], a0, i32x4{0, 0, 0, 0}));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) facc[j][r] = __builtin_fmaf(static_cast<float>(t[r]), bs.scale, facc[j][r]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int ku = k + u * kStep;
+        if (ku >= k1) break;
+        uint4 a;
+        if constexpr (M == kGateUp) {
+          const uint4* v = reinterpret_cast<const uint4*>(xr + ku);
+          a = bf16_codes(v[0], v[1], qs);
+        } else {
+          a = *reinterpret_cast<const uint4*>(p.a + static_cast<size_t>(src) * K + ku + 16 * q);
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[j] = mfma_i8(w[u][j], a, acc[j]);
+      }
+    }
+  }
+  // join: float sums in wave order, so that a result does not depend on timing; wave j
+  // takes column block j
+#pragma unroll
+  for (int j = 0; j < NF; ++j) part[wave][j][lane] = M == kDown ? __builtin_bit_cast(i32x4, facc[j % NC]) : acc[j];
+  __syncthreads();
+  if (wave >= NC || l16 >= it.rows) return;
+  auto joined = [&](int j) MOE_INLINE {
+    f32x4 v;
+    if constexpr (M == kDown) {
+      v = __builtin_bit_cast(f32x4, part[0][j][lane]);
+#pragma unroll
+      for (int i = 1; i < kSplit; ++i) v += __builtin_bit_cast(f32x4, part[i][j][lane]);
+    } else {
+      i32x4 t = part[0][j][lane];
+#pragma unroll
+      for (int i = 1; i < kSplit; ++i) t += part[i][j][lane];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = static_cast<float>(t[r]);
+    }
+    return v;
+  };
+  const int n = (it.chunk * NC + wave) * 16 + 4 * q;
+  const size_t so = static_cast<size_t>(it.expert) * cols + n;
+  const f32x4 s0 = *reinterpret_cast<const f32x4*>(p.s0 + so), g = joined(wave);
+  float v[4];
+  if constexpr (M == kGateUp) {
+    const f32x4 s1 = *reinterpret_cast<const f32x4*>(p.s1 + so), u = joined(NC + wave);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = silu_mul(g[r] * (qs.scale * s0[r]), u[r] * (qs.scale * s1[r]));
+  } else {
+    const float sx = M == kLinear ? p.as[src] : 1.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = g[r] * (sx * s0[r]);
+  }
+  store4(static_cast<Out*>(p.out) + static_cast<size_t>(row) * cols + n, v);
 }
 
 // ---- large groups: LDS-tiled products ----------------------------------------------
@@ -811,6 +994,32 @@ using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves
 constexpr int kTileMinAvg = 48;
 constexpr int kTileMinK = 4 * kStep;   // the row list of a tile is loaded a tile ahead: at least STAGES - 1 steps
 
+// Few rows: so few that items of 128 columns (of at most one 16-row tile per row) would
+// not occupy the chip.
+constexpr int kFewItems = 160;
+constexpr int kFewBlocks = 384;
+bool few(int n_rows, int cols) { return static_cast<long long>(n_rows) * ((cols + kBlock - 1) / kBlock) <= kFewItems; }
+
+// m-tiles of BM rows of a call, at most: ceil(n / BM) <= 1 + (n - 1) / BM for each group with rows.
+int max_m_tiles(const ProductArgs& p, int BM) {
+  const int groups = p.G < p.n_rows ? p.G : p.n_rows;
+  return groups + (p.n_rows - groups) / BM;
+}
+
+template <Mode M, class Out>
+void launch_few(const ProductArgs& p, hipStream_t stream) {
+  const int tiles = max_m_tiles(p, 16), blocks16 = tiles * (p.cols / 16);
+  auto grid = [&](int nc) { return dim3(item_grid(tiles, p.cols / (16 * nc))); };
+  // wider items where 16 columns give more blocks than run at once (a block is mostly waits:
+  // 1024 of them took 10.7 us for one token's down product, 256 of 64 columns 5 us)
+  if (blocks16 <= kFewBlocks)
+    hipLaunchKernelGGL((few_i8<1, M, Out>), grid(1), dim3(kThreadsS), 0, stream, p);
+  else if (M == kGateUp || blocks16 <= 2 * kFewBlocks)
+    hipLaunchKernelGGL((few_i8<2, M, Out>), grid(2), dim3(kThreadsS), 0, stream, p);
+  else
+    hipLaunchKernelGGL((few_i8<M == kGateUp ? 2 : 4, M, Out>), grid(4), dim3(kThreadsS), 0, stream, p);
+}
+
 template <Mode M, class Out>
 void launch_product(const ProductArgs& p, hipStream_t stream) {
   const int avg = p.n_rows / p.G;
@@ -829,8 +1038,7 @@ void launch_product(const ProductArgs& p, hipStream_t stream) {
     return;
   }
   const int mf = pick_mf(avg);
-  const int max_tiles = (p.n_rows + 16 * mf - 1) / (16 * mf) + p.G;
-  dim3 grid(item_grid(max_tiles, (p.cols + kBlock - 1) / kBlock)), block(kThreadsS);
+  dim3 grid(item_grid(max_m_tiles(p, 16 * mf), (p.cols + kBlock - 1) / kBlock)), block(kThreadsS);
   switch (mf) {
     case 1: hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p); break;
     case 2: hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p); break;
@@ -861,7 +1069,7 @@ FfnI8Layout ffn_i8_layout(int n_rows, int n_tokens, int d, int I) {
   FfnI8Layout L;
   L.xs = up(static_cast<size_t>(n_tokens) * d);
   L.aq = L.xs + up(static_cast<size_t>(n_tokens) * 4);
-  L.as = L.aq + up(static_cast<size_t>(n_rows) * I);
+  L.as = L.aq + up(static_cast<size_t>(n_rows) * I * (few(n_rows, I) ? 4 : 1));   // few rows: in fp32
   L.total = L.as + up(static_cast<size_t>((I + kBlock - 1) / kBlock) * n_rows * 4);
   return L;
 }
@@ -876,6 +1084,11 @@ hipError_t launch_grouped_linear_i8(const GroupedI8& g, const int8_t* xq, const 
   p.w0 = w;
   p.s0 = ws;
   p.out = y;
+  if (few(g.n_rows, O)) {
+    if (bf16) launch_few<kLinear, uint16_t>(p, stream);
+    else launch_few<kLinear, float>(p, stream);
+    return hipGetLastError();
+  }
   if (bf16) launch_product<kLinear, uint16_t>(p, stream);
   else launch_product<kLinear, float>(p, stream);
   return hipGetLastError();
@@ -888,6 +1101,23 @@ size_t ffn_i8_workspace_bytes(int n_rows, int n_tokens, int d, int I) {
 hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream) {
   char* ws = static_cast<char*>(workspace);
   const FfnI8Layout L = ffn_i8_layout(a.g.n_rows, a.g.n_x, a.d, a.I);
+  if (few(a.g.n_rows, a.I)) {
+    ProductArgs p = product_args(a.g, a.d, a.I);
+    p.x = a.x;
+    p.w0 = a.w_gate;
+    p.w1 = a.w_up;
+    p.s0 = a.s_gate;
+    p.s1 = a.s_up;
+    p.out = ws + L.aq;
+    launch_few<kGateUp, float>(p, stream);
+    ProductArgs h = product_args(a.g, a.I, a.d);
+    h.af = reinterpret_cast<const float*>(ws + L.aq);
+    h.w0 = a.w_down;
+    h.s0 = a.s_down;
+    h.out = a.h_sorted;
+    launch_few<kDown, uint16_t>(h, stream);
+    return hipGetLastError();
+  }
   int8_t* xq = reinterpret_cast<int8_t*>(ws);
   float* xs = reinterpret_cast<float*>(ws + L.xs);
   const hipError_t e = launch_quantize_rows(a.x, 1, a.g.n_x, a.d, xq, xs, stream);
