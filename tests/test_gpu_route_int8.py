@@ -331,6 +331,66 @@ def test_ffn_parity(name, d, I):
     assert torch.equal(h, h2)
 
 
+# sizes at which the calls run on the LDS-tiled kernels (several tiles per block, partial ones, 128- and 256-row tiles)
+LARGE = {
+    "ragged": dict(sizes=[1, 0, 255, 256, 257, 129, 700, 40, 2000, 16, 1500, 33], T=900),
+    "many": dict(sizes=[100 + 7 * (i % 13) for i in range(44)], T=700),
+    "hot": dict(sizes=[0, 13100, 0, 300], T=2048),
+    "priority": dict(sizes=[600, 0, 1, 900, 1300], T=800, prio_sizes=[64, 3, 0, 130, 1000], shared=1),
+}
+
+
+@pytest.mark.parametrize("name", LARGE)
+@pytest.mark.parametrize("K,O,dtype", [(256, 1344, "f32"), (320, 1344, "bf16"), (704, 1280, "bf16")])
+def test_linear_large(name, K, O, dtype):
+    announce(f"linear large {name} {K} {O} {dtype}")
+    g = _gen(K + O + len(name))
+    b = LARGE[name]
+    rows, offs, E, nseg = _batch(g, **b)
+    S = b.get("shared", 0)
+    xq, xs = _codes(g, b["T"], K), torch.rand(b["T"], generator=g) + 0.1
+    w, ws = _codes(g, E + S, O, K), torch.rand((E + S, O), generator=g) + 0.1
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    args = [t.to(DEV) for t in (xq, xs, offs)] + [E, S, nseg, moe.pack_i8_codes(w).to(DEV), ws.to(DEV)]
+    y = moe.grouped_linear_i8(*args, x_rows=rows.to(DEV), out_dtype=dt)
+    torch.cuda.synchronize()
+    ref = Q.grouped_linear(xq.numpy(), xs.numpy(), rows.numpy(), offs.tolist(), E, nseg, w.numpy(), ws.numpy())
+    tol = (3 * 2.0 ** -24 + torch.finfo(dt).eps / 2) * (1 + 1e-6)
+    assert np.all(np.abs(f64_of(y) - ref) <= tol * np.abs(ref))
+    again = moe.grouped_linear_i8(*args, x_rows=rows.to(DEV), out_dtype=dt)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("name", LARGE)
+@pytest.mark.parametrize("d,I", [(320, 960), (1344, 704)])
+def test_ffn_large(name, d, I):
+    announce(f"ffn large {name} {d} {I}")
+    g = _gen(d + I + len(name))
+    rows, offs, E, nseg, S, x, ws, ss = _ffn_case(g, LARGE[name], d, I)
+    args = _ffn_args(ws, ss)
+    h = moe.grouped_ffn_i8(x.to(DEV), offs.to(DEV), E, S, nseg, *args, x_rows=rows.to(DEV))
+    torch.cuda.synchronize()
+    _ffn_check(f64_of(h), x, rows, offs, E, nseg, ws, ss)
+    again = moe.grouped_ffn_i8(x.to(DEV), offs.to(DEV), E, S, nseg, *args, x_rows=rows.to(DEV))
+    assert torch.equal(h, again)
+
+
+def test_linear_few_hundred_groups():
+    """More groups than the 128-row tiles' lists hold (the 256-row ones take them), and their largest number."""
+    g = _gen(15)
+    for E, nseg in ((512, 1), (512, 2)):
+        sizes = torch.randint(40, 80, (E,), generator=g).tolist()
+        b = dict(sizes=sizes, T=300, **({"prio_sizes": torch.randint(0, 60, (E,), generator=g).tolist()} if nseg == 2 else {}))
+        rows, offs, E, nseg = _batch(g, **b)
+        K, O = 256, 256
+        xq, xs = _codes(g, 300, K), torch.rand(300, generator=g) + 0.1
+        w, ws = _codes(g, E, O, K), torch.rand((E, O), generator=g) + 0.1
+        y = moe.grouped_linear_i8(xq.to(DEV), xs.to(DEV), offs.to(DEV), E, 0, nseg, moe.pack_i8_codes(w).to(DEV), ws.to(DEV),
+                                  x_rows=rows.to(DEV), out_dtype=torch.float32)
+        ref = Q.grouped_linear(xq.numpy(), xs.numpy(), rows.numpy(), offs.tolist(), E, nseg, w.numpy(), ws.numpy())
+        assert np.all(np.abs(f64_of(y) - ref) <= 4 * 2.0 ** -24 * np.abs(ref))
+
+
 def test_ffn_bad_rows_stay_in_their_rows():
     """NaN and infinities in a token row make its outputs NaN and no others; so does a list entry out of range reach
     no memory outside the tokens (it is held to the last token)."""
@@ -396,6 +456,41 @@ def test_route_to_ffn_graph_and_streams(name):
             outs.append(moe.grouped_ffn_i8(xd, od, E, S, nseg, *args, x_rows=rd))
     torch.cuda.synchronize()
     assert torch.equal(outs[0], h) and torch.equal(outs[1], h)
+
+
+@pytest.mark.parametrize("T,prio,S,fused", [(48, 0, 1, True), (300, 16, 0, True), (7, 0, 0, False)])
+def test_layer_with_routing_and_int8_experts(T, prio, S, fused):
+    """MoeLayer with both: its gate is route()'s, its FFN grouped_ffn_i8's, eagerly and through bound_calls."""
+    import workloads
+    wl = workloads.custom(T=T, E=16, k=4, d=256, I=192, dtype="bf16", S=S, n_priority=prio, seed=3, device=DEV)
+    s = wl.spec
+    q = []
+    for w in (wl.w_gate, wl.w_up, wl.w_down):
+        c, sc = moe.quantize_rows_i8(w)
+        q += [moe.pack_i8_codes(c), sc]
+    bias = (torch.randn(16, generator=_gen(16)) * 0.1).to(DEV)
+    routing = dict(score="sigmoid", bias=bias, n_groups=4, top_groups=2, group_rank="top2", scale=2.5)
+    layer = moe.MoeLayer(s.E, s.k, s.d, s.I, s.T, torch.bfloat16, None, None, None, n_shared=S, n_priority=prio, device=DEV,
+                         fused_gather=fused, int8_weights=tuple(q), routing=routing)
+    y = layer.forward(wl.logits, wl.x).clone()
+    ids, w = Q.route(f64_of(wl.logits), 4, "sigmoid", f64_of(bias), 4, 2, "top2", True, 2.5)
+    np.testing.assert_array_equal(np_of(layer.topk_ids), ids)
+    p = moe.permute(layer.topk_ids, 16, S, prio)
+    h = moe.grouped_ffn_i8(wl.x, p["group_offsets"], 16, S, 2 if prio else 1, *q, x_rows=p["sorted_token"])
+    assert torch.equal(h, layer.h_sorted)
+    assert torch.equal(y, moe.combine(h, p["flat_to_sorted"], layer.topk_w, S))
+    # against the layer on the weights that the codes stand for: a few per cent (8-bit steps of rows and blocks)
+    full = [(moe.quantize_rows_i8(t)[0].float() * moe.quantize_rows_i8(t)[1].unsqueeze(-1)).bfloat16() for t in (wl.w_gate, wl.w_up, wl.w_down)]
+    h16 = moe.grouped_ffn(wl.x, p["group_offsets"], 16, S, 2 if prio else 1, *full, x_rows=p["sorted_token"])
+    assert (h.float() - h16.float()).norm() < 0.05 * h16.float().norm()
+    layer.y.zero_()
+    for name, fn, a in layer.bound_calls(wl.logits, wl.x):
+        assert fn(*a) == 0, name
+    torch.cuda.synchronize()
+    assert torch.equal(layer.y, y)
+    for bad in (dict(routing=dict(scores="sigmoid")), dict(int8_weights=tuple(q), fused_combine=True)):
+        with pytest.raises(ValueError):
+            moe.MoeLayer(s.E, s.k, s.d, s.I, s.T, torch.bfloat16, None, None, None, device=DEV, **bad)
 
 
 def test_bindings_refuse_mismatches():

@@ -746,7 +746,8 @@ class MoeLayer:
 
     def __init__(self, E, k, d, I, T, dtype, w_gate, w_up, w_down, n_shared=0, n_priority=0,
                  renormalize=True, stats_layers=0, req_offsets=None, device="cuda", topk_ids=None,
-                 fused_gather=True, w_router=None, fp8_weights=None, packed_weights=False, fused_combine=False):
+                 fused_gather=True, w_router=None, fp8_weights=None, packed_weights=False, fused_combine=False,
+                 int8_weights=None, routing=None):
         dev = torch.device(device)
         # fp8_weights = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down):
         # the FFN runs moe_grouped_ffn_fp8w on them instead of w_gate / w_up / w_down
@@ -760,6 +761,17 @@ class MoeLayer:
         self.fused_combine = bool(fused_combine)
         if self.fused_combine and (fp8_weights is not None or dtype != torch.bfloat16):
             raise ValueError("fused_combine serves bf16 expert weights only")
+        # int8_weights = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down), codes from
+        # pack_i8_codes: the FFN runs moe_grouped_ffn_i8 on them instead of w_gate / w_up / w_down
+        self.int8_weights = int8_weights
+        if int8_weights is not None and (fp8_weights is not None or self.fused_combine or dtype != torch.bfloat16):
+            raise ValueError("int8_weights serve bf16 tokens, without fp8_weights or fused_combine")
+        # routing: None (moe_gate), or a dict of route()'s score, bias, n_groups, top_groups, group_rank, scale:
+        # the layer's gate is moe_route
+        self.routing = None if routing is None else dict(routing)
+        unknown = set(self.routing or ()) - {"score", "bias", "n_groups", "top_groups", "group_rank", "scale"}
+        if unknown:
+            raise ValueError(f"unknown routing options {sorted(unknown)}")
         self.w_router = w_router
         self.logits = torch.empty((T, E), dtype=torch.float32, device=dev) if w_router is not None else None
         self.E, self.k, self.d, self.I, self.T = E, k, d, I, T
@@ -788,6 +800,8 @@ class MoeLayer:
         self.h_sorted = torch.empty((N, d), dtype=dtype, device=dev)
         if self.fused_combine:
             ws_bytes = ffn_combine_workspace_bytes(N, E, n_shared, self.nseg, d, I, T, k, self.packed)
+        elif int8_weights is not None:
+            ws_bytes = ffn_i8_workspace_bytes(N, T if fused_gather else 0, d, I, E, n_shared, self.nseg)
         elif fp8_weights is not None:
             ws_bytes = ffn_fp8w_workspace_bytes(N, I, E, n_shared, self.nseg, d, self.packed)
         else:
@@ -806,6 +820,9 @@ class MoeLayer:
         return router(x, self.w_router, self.logits)
 
     def gate(self, logits):
+        if self.routing is not None:
+            return route(logits, self.k, renormalize=self.renormalize, topk_ids=self.topk_ids, topk_w=self.topk_w,
+                         **self.routing)
         return gate(logits, self.k, self.renormalize, self.topk_ids, self.topk_w)
 
     def permute(self, x):
@@ -820,6 +837,11 @@ class MoeLayer:
                                    packed=self.packed)
 
     def ffn(self, x):
+        if self.int8_weights is not None:
+            src = x if self.fused_gather else self.perm["x_sorted"]
+            return grouped_ffn_i8(src, self.perm["group_offsets"], self.E, self.S, self.nseg, *self.int8_weights,
+                                  h_sorted=self.h_sorted, workspace=self.ffn_ws,
+                                  x_rows=self.perm["sorted_token"] if self.fused_gather else None)
         if self.fp8_weights is not None:
             src = x if self.fused_gather else self.perm["x_sorted"]
             return grouped_ffn_fp8w(src, self.perm["group_offsets"], self.E, self.S, self.nseg, *self.fp8_weights,
@@ -867,8 +889,7 @@ class MoeLayer:
             calls.append(("moe_router", lib.moe_router, (x.data_ptr(), self.w_router.data_ptr(), T, self.d, E, dt,
                                                          logits.data_ptr(), st)))
         calls += [
-            ("moe_gate", lib.moe_gate, (logits.data_ptr(), T, E, k, int(bool(self.renormalize)),
-                                        self.topk_ids.data_ptr(), self.topk_w.data_ptr(), st)),
+            self._gate_call(lib, logits, st),
             ("moe_permute", lib.moe_permute, (self.topk_ids.data_ptr(), T, E, k, self.S, self.P,
                                               None if fused else x.data_ptr(), dt,
                                               self.d, self.perm["group_offsets"].data_ptr(),
@@ -908,10 +929,27 @@ class MoeLayer:
         self._keep = (n_perm, n_ffn, n_st if stats_ids is not None and self.stats_out is not None else None)
         return calls
 
+    def _gate_call(self, lib, logits, st):
+        if self.routing is None:
+            return ("moe_gate", lib.moe_gate, (logits.data_ptr(), self.T, self.E, self.k, int(bool(self.renormalize)),
+                                               self.topk_ids.data_ptr(), self.topk_w.data_ptr(), st))
+        o = {"score": "softmax", "bias": None, "n_groups": 1, "top_groups": None, "group_rank": "max", "scale": 1.0,
+             **self.routing}
+        groups = o["n_groups"]
+        return ("moe_route", lib.moe_route, (
+            logits.data_ptr(), _dtype_code(logits), _ptr(o["bias"]), self.T, self.E, self.k, _lib.SCORES[o["score"]],
+            groups, groups if o["top_groups"] is None else o["top_groups"], _lib.GROUP_RANKS[o["group_rank"]],
+            int(bool(self.renormalize)), float(o["scale"]), self.topk_ids.data_ptr(), self.topk_w.data_ptr(), st))
+
     def _ffn_call(self, lib, x, fused, dt, n_ffn, st):
         src = x.data_ptr() if fused else self.perm["x_sorted"].data_ptr()
         rows = self.perm["sorted_token"].data_ptr() if fused else None
         offs = self.perm["group_offsets"].data_ptr()
+        if self.int8_weights is not None:
+            qg, sg, qu, su, qd, sd = (t.data_ptr() for t in self.int8_weights)
+            return ("moe_grouped_ffn_i8", lib.moe_grouped_ffn_i8, (
+                src, rows, self.T, offs, self.N, self.E, self.S, self.nseg, self.d, self.I, qg, sg, qu, su, qd, sd,
+                self.h_sorted.data_ptr(), self.ffn_ws.data_ptr(), ctypes.byref(n_ffn), st))
         if self.fp8_weights is not None:
             qg, sg, qu, su, qd, sd = (t.data_ptr() for t in self.fp8_weights)
             name = "moe_grouped_ffn_fp8w_packed" if self.packed else "moe_grouped_ffn_fp8w"

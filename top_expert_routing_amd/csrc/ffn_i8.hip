@@ -863,12 +863,12 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
         for (int i = 0; i < MI; ++i) {
 #pragma unroll
           for (int j = i * NJ / MI; j < (i + 1) * NJ / MI; ++j) bn[j] = bfrag(st, 0, j);
-#pragma unroll
-          for (int l = i * PER / MI; l < (i + 1) * PER / MI; ++l) load(l);
           if (i < n) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_i8(b[j], fa[i], acc[i][j]);
           }
+#pragma unroll
+          for (int l = i * PER / MI; l < (i + 1) * PER / MI; ++l) load(l);
           fa[i] = afrag(st, 0, i);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -977,6 +977,7 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+// Rows of stream_i8's tiles, 16 * mf: groups of the average size in one tile.
 int pick_mf(int avg) { return avg <= 12 ? 1 : avg <= 28 ? 2 : 4; }
 
 // CUs of the current device.
@@ -989,15 +990,28 @@ int device_cus() {
 }
 
 using TileWide = TileCfg<4, 8, 4, 2, 1>;   // 256 rows, one block of eight waves per CU
-using TileDown = TileCfg<4, 8, 4, 2, 1>;
 using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves per CU
-constexpr int kTileMinAvg = 48;
-constexpr int kTileMinK = 4 * kStep;   // the row list of a tile is loaded a tile ahead: at least STAGES - 1 steps
+using TileDown = TileWide;
 
-// Few rows: so few that items of 128 columns (of at most one 16-row tile per row) would
-// not occupy the chip.
-constexpr int kFewItems = 160;
-constexpr int kFewBlocks = 384;
+// Which kernel: the host sees the average group, not the groups.  Times of the whole call,
+// us; d, I or K, O = 2048, 1024 (FFN, 64 groups) and 2048, 2048 (linear, one group).
+//   few_i8 or stream_i8     linear 128 rows 6.9 / 11.6, 256 rows 11.3 / 11.7: few_i8 up to
+//                           kFewBlocksMost items of 16 x 16.  FFN of one token (8 rows)
+//                           19 / 20; 16 groups of one row, 1024 x 512, 12.7 / 14.6, of 8
+//                           rows 15.3 / 15.4; 64 groups of one row 137 / 80: only up to
+//                           kFewItems items of 128 columns, which also bounds the fp32
+//                           product to 80 KiB.
+//   stream_i8 or tile_i8    64 rows a group 124 / 118, 96 rows 167 / 127; but linear 2048
+//                           rows (512 items of 64 x 128) 20 / 24, 4096 rows 40 / 30, 16
+//                           groups of 256 rows, 1024 x 512 (256 items) 37 / 44: tile_i8
+//                           needs both full tiles and enough of them.
+//   TileHalf or TileWide    128 rows a group 136 / 142, 192 rows 163 / 158; linear 4096 rows
+//                           (128 wide tiles) 30 / 34, 8191 x 4096 (512) 85 / 79.
+constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
+constexpr int kTileMinAvg = 48, kTileMinItems = 640;
+constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
+constexpr int kWideMinAvg = 192, kWideMinTiles = 256;
+
 bool few(int n_rows, int cols) { return static_cast<long long>(n_rows) * ((cols + kBlock - 1) / kBlock) <= kFewItems; }
 
 // m-tiles of BM rows of a call, at most: ceil(n / BM) <= 1 + (n - 1) / BM for each group with rows.
@@ -1020,21 +1034,26 @@ void launch_few(const ProductArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL((few_i8<M == kGateUp ? 2 : 4, M, Out>), grid(4), dim3(kThreadsS), 0, stream, p);
 }
 
+template <class Tile, Mode M, class Out>
+void launch_tile(const ProductArgs& p, hipStream_t stream) {
+  const int cus = (device_cus() + kXcds - 1) / kXcds * kXcds;
+  const size_t lds = TileLds<Tile, M>::bytes(p.G);
+  hipLaunchKernelGGL((tile_i8<Tile, M, Out>), dim3(cus * Tile::BPC), dim3(Tile::NT), lds, stream, p);
+}
+
 template <Mode M, class Out>
 void launch_product(const ProductArgs& p, hipStream_t stream) {
   const int avg = p.n_rows / p.G;
-  if (avg > kTileMinAvg && p.K >= kTileMinK) {
-    const int cus = (device_cus() + kXcds - 1) / kXcds * kXcds;
-    if constexpr (M != kDown) {
-      const size_t lds = TileLds<TileHalf, M>::bytes(p.G);
-      if (lds <= kLdsPerCu / 2) {
-        hipLaunchKernelGGL((tile_i8<TileHalf, M, Out>), dim3(2 * cus), dim3(TileHalf::NT), lds, stream, p);
-        return;
-      }
+  const long long area = static_cast<long long>(p.n_rows) * p.cols;
+  if (avg > kTileMinAvg && p.K >= kTileMinK && area >= kTileMinItems * 64ll * 128) {
+    const long long wide = area / (256 * (M == kGateUp ? 128 : 256));
+    // (the lists of two blocks per CU have room for some 380 groups)
+    if (M == kDown || (avg >= kWideMinAvg && wide >= kWideMinTiles) ||
+        TileLds<TileHalf, M == kDown ? kLinear : M>::bytes(p.G) > kLdsPerCu / 2) {
+      launch_tile<std::conditional_t<M == kDown, TileDown, TileWide>, M, Out>(p, stream);
+    } else if constexpr (M != kDown) {
+      launch_tile<TileHalf, M, Out>(p, stream);
     }
-    using Tile = std::conditional_t<M == kDown, TileDown, TileWide>;
-    const size_t lds = TileLds<Tile, M>::bytes(p.G);
-    hipLaunchKernelGGL((tile_i8<Tile, M, Out>), dim3(cus * Tile::BPC), dim3(Tile::NT), lds, stream, p);
     return;
   }
   const int mf = pick_mf(avg);
@@ -1084,7 +1103,7 @@ hipError_t launch_grouped_linear_i8(const GroupedI8& g, const int8_t* xq, const 
   p.w0 = w;
   p.s0 = ws;
   p.out = y;
-  if (few(g.n_rows, O)) {
+  if (static_cast<long long>(max_m_tiles(p, 16)) * (O / 16) <= kFewBlocksMost) {
     if (bf16) launch_few<kLinear, uint16_t>(p, stream);
     else launch_few<kLinear, float>(p, stream);
     return hipGetLastError();
