@@ -2,10 +2,11 @@
 //
 // One pass: a row's values are loaded once, all loads of a lane in flight
 // together, stay in registers through the maximum, and leave as codes.  Bound by
-// memory: 3 (bf16) or 5 (fp32) bytes a value.  A wavefront takes a row; where
-// there are too few rows to fill the chip so, a block of four wavefronts does, which
-// cuts the chain of a row's loads and roundings by four (one row of 2048: 6.3 us
-// with one wavefront).  Rows of more than 64 (256) * 8 * kMaxHeld values are read twice.
+// memory: 3 (bf16) or 5 (fp32) bytes a value.  A block of four wavefronts takes a row,
+// or, where a row has no more values than the loads of one wavefront, each
+// wavefront one.  (A wavefront per row at every size: bf16 4096 x 2048 9.8 us against 8.1,
+// 8192 x 2880 21.2 us against 17.5, which is 4.04 TB/s; a row's loads and roundings are
+// one chain.)  Rows of more than 256 * 8 * kMaxHeld values are read twice.
 #include "launch.h"
 #include "quantize.h"
 
@@ -90,30 +91,28 @@ __global__ __launch_bounds__(kThreads) void quantize_rows(const void* __restrict
   if (l == 0) s[t] = qs.scale;
 }
 
-template <bool BF16, int LANES>
-void launch_lanes(const void* x, int T, int d, int8_t* q, float* s, hipStream_t stream) {
-  const int pieces = (d / 8 + LANES - 1) / LANES;
-  dim3 grid((T + kThreads / LANES - 1) / (kThreads / LANES)), block(kThreads);
-  if (pieces <= 1) hipLaunchKernelGGL((quantize_rows<BF16, LANES, 1>), grid, block, 0, stream, x, T, d, q, s);
-  else if (pieces <= 2) hipLaunchKernelGGL((quantize_rows<BF16, LANES, 2>), grid, block, 0, stream, x, T, d, q, s);
-  else if (pieces <= 4) hipLaunchKernelGGL((quantize_rows<BF16, LANES, 4>), grid, block, 0, stream, x, T, d, q, s);
-  else if (pieces <= kMaxHeld) hipLaunchKernelGGL((quantize_rows<BF16, LANES, kMaxHeld>), grid, block, 0, stream, x, T, d, q, s);
-  else hipLaunchKernelGGL((quantize_rows<BF16, LANES, 0>), grid, block, 0, stream, x, T, d, q, s);
+template <bool BF16>
+void launch_rows(const void* x, int T, int d, int8_t* q, float* s, hipStream_t stream) {
+  dim3 block(kThreads);
+  if (d <= kWave * 8) {
+    const dim3 grid((T + kThreads / kWave - 1) / (kThreads / kWave));
+    hipLaunchKernelGGL((quantize_rows<BF16, kWave, 1>), grid, block, 0, stream, x, T, d, q, s);
+    return;
+  }
+  const int pieces = (d / 8 + kThreads - 1) / kThreads;
+  const dim3 grid(T);
+  if (pieces <= 1) hipLaunchKernelGGL((quantize_rows<BF16, kThreads, 1>), grid, block, 0, stream, x, T, d, q, s);
+  else if (pieces <= 2) hipLaunchKernelGGL((quantize_rows<BF16, kThreads, 2>), grid, block, 0, stream, x, T, d, q, s);
+  else if (pieces <= 4) hipLaunchKernelGGL((quantize_rows<BF16, kThreads, 4>), grid, block, 0, stream, x, T, d, q, s);
+  else if (pieces <= kMaxHeld) hipLaunchKernelGGL((quantize_rows<BF16, kThreads, kMaxHeld>), grid, block, 0, stream, x, T, d, q, s);
+  else hipLaunchKernelGGL((quantize_rows<BF16, kThreads, 0>), grid, block, 0, stream, x, T, d, q, s);
 }
-
-// Rows from which a wavefront per row fills the chip (256 CUs, eight rows each).
-constexpr int kManyRows = 2048;
 
 }  // namespace
 
 hipError_t launch_quantize_rows(const void* x, int bf16, int T, int d, int8_t* q, float* s, hipStream_t stream) {
-  if (T >= kManyRows) {
-    if (bf16) launch_lanes<true, kWave>(x, T, d, q, s, stream);
-    else launch_lanes<false, kWave>(x, T, d, q, s, stream);
-  } else {
-    if (bf16) launch_lanes<true, kThreads>(x, T, d, q, s, stream);
-    else launch_lanes<false, kThreads>(x, T, d, q, s, stream);
-  }
+  if (bf16) launch_rows<true>(x, T, d, q, s, stream);
+  else launch_rows<false>(x, T, d, q, s, stream);
   return hipGetLastError();
 }
 
