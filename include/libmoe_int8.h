@@ -65,8 +65,8 @@ moe_status moe_quantize_rows_i8(const void* x, moe_dtype dtype, int32_t T, int32
  *            an ordinary linear map.
  *   w        [E+n_shared][O][K] int8, packed (above).  w_scale [E+n_shared][O].
  *   y        [n_rows][O] of `out_dtype` (bf16 or fp32), written.
- *   Requires K and O positive multiples of 64, K <= 131072 (the sums stay in
- *   int32), nseg in {1, 2}, 1 <= E <= 512, n_shared <= 256; tensors of codes and
+ *   Requires K and O positive multiples of 64, K <= 131072 (the sums of codes in
+ *   [-127, 127] stay in int32), nseg in {1, 2}, 1 <= E <= 512, n_shared <= 256; tensors of codes and
  *   values 16-byte aligned, w_scale 16-byte, x_scale 4-byte.
  *   Errors: MOE_ERR_INVALID_ARG for negative sizes, nseg, NULL or misaligned
  *   pointers, n_x < 1 with a row list; MOE_ERR_UNSUPPORTED for the other
@@ -85,15 +85,22 @@ moe_status moe_grouped_linear_i8(const int8_t* xq, const float* x_scale, const i
  *     a = silu(g) * u in fp32, quantised per row and MOE_I8_BLOCK columns -> aq, sa
  *     h = s_down * sum over the blocks b of sa[b] * (aq . W_down over b)  (fp32 over the
  *         blocks, exact int32 inside one), rounded once to bf16.
+ * A block of the SwiGLU product whose scale is below 2^-126 counts as zeros.
+ * silu uses the hardware's exponential and reciprocal (2 ulp each), and a code
+ * whose quotient lies within 1e-4 of a border may be the neighbour.
  *
  *   x_sorted, x_rows, n_x, group_offsets, n_rows, E, n_shared, nseg, h_sorted: as
- *                  moe_grouped_ffn with dtype MOE_BF16; each token row is
- *                  quantised once, also where several sorted rows read it.
+ *                  moe_grouped_ffn with dtype MOE_BF16.  All n_x token rows are
+ *                  quantised, once each however many sorted rows read them (a
+ *                  batch of few rows quantises them where it multiplies).
  *   w_gate, w_up   [E+n_shared][I][d] int8, packed; s_gate, s_up [E+n_shared][I].
  *   w_down         [E+n_shared][d][I] int8, packed; s_down [E+n_shared][d].
- *   workspace      of the queried size; it depends on n_rows, n_x (where a row
- *                  list is given; the query takes x_rows' presence from n_x > 0),
- *                  d and I only.
+ *   workspace      of the queried size, whose contents need no preparation: the
+ *                  token codes and scales, the SwiGLU product in codes and block
+ *                  scales (few rows: in fp32).  The size depends on n_rows, n_x
+ *                  (where a row list is given; the query takes x_rows' presence
+ *                  from n_x > 0), d and I only.  Calls that share a workspace,
+ *                  replayed graphs among them, must not overlap in time.
  *   Requires d and I positive multiples of 64, d <= 131072.
  *   Errors: as moe_grouped_ffn_fp8w_packed.
  */

@@ -526,3 +526,56 @@ def test_bindings_refuse_mismatches():
             moe.route(l, 2, **kw)
     with pytest.raises(TypeError):
         moe.route(l.half(), 2)
+
+
+# ------------------------------------------------------------------ the largest sizes
+def test_ffn_most_groups():
+    """512 experts in two segments and 256 shared ones, each group of a few tens of rows, on the LDS-tiled kernels."""
+    announce("ffn most groups")
+    g = _gen(18)
+    sizes = lambda: torch.randint(0, 140, (512,), generator=g).tolist()
+    d, I = 256, 256
+    rows, offs, E, nseg, S, x, ws, ss = _ffn_case(g, dict(sizes=sizes(), prio_sizes=sizes(), T=53, shared=256), d, I)
+    h = moe.grouped_ffn_i8(x.to(DEV), offs.to(DEV), E, S, nseg, *_ffn_args(ws, ss), x_rows=rows.to(DEV))
+    torch.cuda.synchronize()
+    _ffn_check(f64_of(h), x, rows, offs, E, nseg, ws, ss)
+
+
+def test_quantize_more_rows_than_one_launch():
+    announce("quantize 2^23 + 77 rows")
+    x = torch.randn((4096, 8), generator=_gen(19)).bfloat16().to(DEV)
+    q0, s0 = moe.quantize_rows_i8(x)
+    T = 2 ** 23 + 77
+    q, s = moe.quantize_rows_i8(x.repeat(2049, 1)[:T].contiguous())
+    assert torch.equal(q, q0.repeat(2049, 1)[:T]) and torch.equal(s, s0.repeat(2049)[:T])
+
+
+def test_route_more_tokens_than_one_launch():
+    announce("route 2^25 + 33 tokens")
+    l = torch.randn((4096, 4), generator=_gen(20)).bfloat16().to(DEV)
+    i0, w0 = moe.route(l, 2, "sigmoid")
+    T = 2 ** 25 + 33
+    i, w = moe.route(l.repeat(8193, 1)[:T].contiguous(), 2, "sigmoid")
+    assert torch.equal(i, i0.repeat(8193, 1)[:T]) and torch.equal(w, w0.repeat(8193, 1)[:T])
+
+
+def test_layer_refuses_what_its_raw_calls_would_read_wrongly():
+    z = lambda *s, dt=torch.int8: torch.zeros(s, dtype=dt, device=DEV)
+    f = torch.float32
+    E, k, d, I, T = 4, 2, 64, 128, 5
+    good = (z(E, I, d), z(E, I, dt=f), z(E, I, d), z(E, I, dt=f), z(E, d, I), z(E, d, dt=f))
+    make = lambda **kw: moe.MoeLayer(E, k, d, I, T, torch.bfloat16, None, None, None, device=DEV, **{"int8_weights": good, **kw})
+    for i, v in ((0, z(E, I, d + 64)), (1, z(E, I - 1, dt=f)), (4, z(E, I, d)), (5, z(E, d))):
+        with pytest.raises((TypeError, ValueError)):
+            make(int8_weights=tuple(v if j == i else t for j, t in enumerate(good)))
+    for r in (dict(bias=z(E - 1, dt=f)), dict(bias=z(E)), dict(score="tanh"), dict(group_rank="mean"), dict(bias=z(E, dt=f).cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            make(routing=r)
+    layer = make(routing=dict(score="sigmoid"))
+    x = z(T, d, dt=torch.bfloat16)
+    layer.bound_calls(z(T, E, dt=f), x)
+    with pytest.raises(ValueError):
+        layer.bound_calls(z(T, E + 1, dt=f), x)
+    layer.int8_weights = good[:5] + (z(E, d - 1, dt=f),)
+    with pytest.raises(ValueError):
+        layer.bound_calls(z(T, E, dt=f), x)

@@ -615,6 +615,20 @@ def ffn_i8_workspace_bytes(n_rows, n_x, d, I, E=1, n_shared=0, nseg=1) -> int:
     return int(n.value)
 
 
+def _need_i8_weights(like: torch.Tensor, G: int, d: int, I: int, weights) -> None:
+    """The six tensors (codes, scales of gate, up, down) of an int8 FFN over G experts."""
+    index = like.get_device()
+    shapes = (("w_gate", torch.int8, (G, I, d)), ("s_gate", torch.float32, (G, I)),
+              ("w_up", torch.int8, (G, I, d)), ("s_up", torch.float32, (G, I)),
+              ("w_down", torch.int8, (G, d, I)), ("s_down", torch.float32, (G, d)))
+    if len(weights) != len(shapes):
+        raise ValueError("int8 weights are codes and scales of gate, up and down")
+    for t, (name, dtype, shape) in zip(weights, shapes):
+        if not _ok(t, index, dtype, shape):
+            _out(t, name, dtype, shape)
+            _same_device(like, **{name: t})
+
+
 def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_shared: int, nseg: int,
                    w_gate: torch.Tensor, s_gate: torch.Tensor, w_up: torch.Tensor, s_up: torch.Tensor,
                    w_down: torch.Tensor, s_down: torch.Tensor, h_sorted: Optional[torch.Tensor] = None,
@@ -633,14 +647,11 @@ def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_share
     if workspace is None:
         workspace = torch.empty(max(ffn_i8_workspace_bytes(N, n_x, d, I, E, n_shared, nseg), 256), dtype=torch.uint8,
                                 device=x.device)
-    need = (("w_gate", w_gate, torch.int8, (G, I, d)), ("s_gate", s_gate, torch.float32, (G, I)),
-            ("w_up", w_up, torch.int8, (G, I, d)), ("s_up", s_up, torch.float32, (G, I)),
-            ("w_down", w_down, torch.int8, (G, d, I)), ("s_down", s_down, torch.float32, (G, d)),
-            ("h_sorted", h_sorted, torch.bfloat16, (N, d)), ("workspace", workspace, torch.uint8, (workspace.numel(),)))
-    for name, t, dtype, shape in need:
-        if not _ok(t, index, dtype, shape):
-            _out(t, name, dtype, shape)
-            _same_device(x, **{name: t})
+    _need_i8_weights(x, G, d, I, (w_gate, s_gate, w_up, s_up, w_down, s_down))
+    if not (_ok(h_sorted, index, torch.bfloat16, (N, d)) and _ok(workspace, index, torch.uint8, (workspace.numel(),))):
+        _out(h_sorted, "h_sorted", torch.bfloat16, (N, d))
+        _out(workspace, "workspace", torch.uint8, (workspace.numel(),))
+        _same_device(x, h_sorted=h_sorted, workspace=workspace)
     nbytes = ctypes.c_size_t(workspace.numel())
     _call("moe_grouped_ffn_i8", index, _lib.load().moe_grouped_ffn_i8, x.data_ptr(), _ptr(x_rows), n_x,
           group_offsets.data_ptr(), N, E, n_shared, nseg, d, I, w_gate.data_ptr(), s_gate.data_ptr(), w_up.data_ptr(),
@@ -772,6 +783,14 @@ class MoeLayer:
         unknown = set(self.routing or ()) - {"score", "bias", "n_groups", "top_groups", "group_rank", "scale"}
         if unknown:
             raise ValueError(f"unknown routing options {sorted(unknown)}")
+        if self.routing and self.routing.get("score", "softmax") not in _lib.SCORES:
+            raise ValueError(f"score must be one of {sorted(_lib.SCORES)}")
+        if self.routing and self.routing.get("group_rank", "max") not in _lib.GROUP_RANKS:
+            raise ValueError(f"group_rank must be one of {sorted(_lib.GROUP_RANKS)}")
+        if self.routing and self.routing.get("bias") is not None:
+            _out(self.routing["bias"], "bias", torch.float32, (E,))
+        if int8_weights is not None:
+            _need_i8_weights(int8_weights[0], E + n_shared, d, I, int8_weights)
         self.w_router = w_router
         self.logits = torch.empty((T, E), dtype=torch.float32, device=dev) if w_router is not None else None
         self.E, self.k, self.d, self.I, self.T = E, k, d, I, T
@@ -936,6 +955,10 @@ class MoeLayer:
         o = {"score": "softmax", "bias": None, "n_groups": 1, "top_groups": None, "group_rank": "max", "scale": 1.0,
              **self.routing}
         groups = o["n_groups"]
+        _need(logits, "logits", None, 2)
+        if tuple(logits.shape) != (self.T, self.E):
+            raise ValueError(f"logits must have shape {(self.T, self.E)}, got {tuple(logits.shape)}")
+        _same_device(logits, bias=o["bias"], topk_ids=self.topk_ids)
         return ("moe_route", lib.moe_route, (
             logits.data_ptr(), _dtype_code(logits), _ptr(o["bias"]), self.T, self.E, self.k, _lib.SCORES[o["score"]],
             groups, groups if o["top_groups"] is None else o["top_groups"], _lib.GROUP_RANKS[o["group_rank"]],
@@ -946,6 +969,7 @@ class MoeLayer:
         rows = self.perm["sorted_token"].data_ptr() if fused else None
         offs = self.perm["group_offsets"].data_ptr()
         if self.int8_weights is not None:
+            _need_i8_weights(self.h_sorted, self.E + self.S, self.d, self.I, self.int8_weights)
             qg, sg, qu, su, qd, sd = (t.data_ptr() for t in self.int8_weights)
             return ("moe_grouped_ffn_i8", lib.moe_grouped_ffn_i8, (
                 src, rows, self.T, offs, self.N, self.E, self.S, self.nseg, self.d, self.I, qg, sg, qu, su, qd, sd,

@@ -111,9 +111,19 @@ void launch_rows(const void* x, int T, int d, int8_t* q, float* s, hipStream_t s
 }  // namespace
 
 hipError_t launch_quantize_rows(const void* x, int bf16, int T, int d, int8_t* q, float* s, hipStream_t stream) {
-  if (bf16) launch_rows<true>(x, T, d, q, s, stream);
-  else launch_rows<false>(x, T, d, q, s, stream);
-  return hipGetLastError();
+  // a grid has fewer than 2^32 threads: at most 2^23 rows of a block each in a launch
+  constexpr int kMost = 1 << 23;
+  for (int t = 0; t < T; t += kMost) {
+    const int n = T - t < kMost ? T - t : kMost;
+    const size_t at = static_cast<size_t>(t) * d;
+    const void* xt = static_cast<const char*>(x) + at * (bf16 ? 2 : 4);
+    if (bf16) launch_rows<true>(xt, n, d, q + at, s + t, stream);
+    else launch_rows<false>(xt, n, d, q + at, s + t, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (n < kMost) break;                       // t + kMost may pass int32
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

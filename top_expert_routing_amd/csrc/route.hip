@@ -307,17 +307,28 @@ hipError_t launch_route(const void* logits, const float* bias, const RouteArgs& 
       break;
     }
   }
-  switch (P) {
-    case 1: launch_p<1>(logits, bias, a, stream); break;
-    case 2: launch_p<2>(logits, bias, a, stream); break;
-    case 3: launch_p<3>(logits, bias, a, stream); break;
-    case 4: launch_p<4>(logits, bias, a, stream); break;
-    case 5: launch_p<5>(logits, bias, a, stream); break;
-    case 6: launch_p<6>(logits, bias, a, stream); break;
-    case 7: launch_p<7>(logits, bias, a, stream); break;
-    default: launch_p<8>(logits, bias, a, stream); break;
+  // a grid has fewer than 2^32 threads: at most 2^25 tokens of a wavefront each in a launch
+  constexpr int kMost = 1 << 25;
+  for (int t = 0; t < args.T; t += kMost) {
+    a.T = args.T - t < kMost ? args.T - t : kMost;
+    a.topk_ids = args.topk_ids + static_cast<size_t>(t) * a.k;
+    a.topk_w = args.topk_w + static_cast<size_t>(t) * a.k;
+    const void* row = static_cast<const char*>(logits) + static_cast<size_t>(t) * a.E * (a.bf16 ? 2 : 4);
+    switch (P) {
+      case 1: launch_p<1>(row, bias, a, stream); break;
+      case 2: launch_p<2>(row, bias, a, stream); break;
+      case 3: launch_p<3>(row, bias, a, stream); break;
+      case 4: launch_p<4>(row, bias, a, stream); break;
+      case 5: launch_p<5>(row, bias, a, stream); break;
+      case 6: launch_p<6>(row, bias, a, stream); break;
+      case 7: launch_p<7>(row, bias, a, stream); break;
+      default: launch_p<8>(row, bias, a, stream); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.T < kMost) break;                     // t + kMost may pass int32
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace moe
