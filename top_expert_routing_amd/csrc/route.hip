@@ -3,14 +3,20 @@
 // token; lane l holds the P experts l * P .. l * P + P - 1 (one 4 * P or 2 * P
 // byte run of the row).
 //
-// Everything that decides an id is computed in double, so that neighbouring
-// scores fall as the definition says; fp64 runs at the fp32 rate here, and a
-// score (an exponential and a division) costs about 45 of the ~700 instructions
-// of a token with 256 experts.  The rest are cross-lane steps, which stay in the
-// vector registers: within 16-lane rows by DPP, across them by lane reads.  A
-// choice value is held as an order-preserving 64-bit key; the maximum over the
-// lanes is taken over the upper halves, and over the lower ones only where
-// several lanes share the upper one.
+// Bound by the vector instructions: a token of 256 experts in 8 groups with a bias
+// (k = 8, sigmoid) issues 625 and 227 scalar ones, so 8192 tokens, eight wavefronts a
+// SIMD, need 8.3 us of the 10.8 measured; 16 tokens take 4.3 us, most of it the launch.
+//   * Everything that decides an id is computed in double, so that neighbouring
+//     scores fall as the definition says; fp64 runs at the fp32 rate here, and a
+//     score (an exponential and a division) costs about 45 instructions a lane.
+//   * Cross-lane steps stay in the vector registers (DPP).  A choice value is held as an
+//     order-preserving 64-bit key; the maximum over the lanes is taken over the upper
+//     halves, and over the lower ones only where several experts share the upper one.
+//   * A round costs 18 vector instructions at P = 4: the masks of the lanes that hold the
+//     maximum retire it and leave its rank in the key's place, so nothing is moved to
+//     other lanes; each lane stores its chosen experts itself.  (Rounds that keep their
+//     winner in lane r and gather its score afterwards: 12.9 us and, bf16, 4159 tokens of
+//     160 experts, 11.0; now 8.8.)
 //   * P is the smallest one that fits whose groups cover whole, power-of-two runs
 //     of lanes (8 groups of 32 experts: P = 4, 8 lanes a group; 8 of 20: P = 5,
 //     4 lanes): the groups' values then come from the same DPP steps.  Other
@@ -26,27 +32,30 @@ namespace {
 
 constexpr int kWavesPerBlock = 4;
 
-// Monotone map of a double to uint64; NaN as -inf, -0 as +0.  0 is below every
-// key it returns and marks experts that cannot be chosen (any more).
+// Monotone map of a double to uint64; NaN as -inf, -0 as +0.  The upper half of
+// every key it returns is above kNoKey; smaller ones mark experts that cannot be
+// chosen (any more).
+constexpr uint32_t kNoKey = 0xffffeu;             // (the key of -inf is 0xfffff ffffffff)
 __device__ __forceinline__ uint64_t key_of(double v) {
-  if (v != v) v = -__builtin_inf();
-  if (v == 0.0) v = 0.0;
+  v = v != v ? -__builtin_inf() : v + 0.0;
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+  const uint32_t hi = static_cast<uint32_t>(u >> 32), sign = static_cast<uint32_t>(static_cast<int32_t>(hi) >> 31);
+  return static_cast<uint64_t>(hi ^ (sign | 0x80000000u)) << 32 | (static_cast<uint32_t>(u) ^ sign);
 }
 
-template <int CTRL>
+// Lane l's value from the lane that CTRL names for it; 0 in the 16-lane rows that ROWS leaves out.
+template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return static_cast<uint32_t>(
-      __builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, 0xf, 0xf, false));
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
 }
-template <int CTRL>
+template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ double dpp(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(u >> 32))) << 32 |
-                                        dpp<CTRL>(static_cast<uint32_t>(u)));
+  return __builtin_bit_cast(double, static_cast<uint64_t>(dpp<CTRL, ROWS>(static_cast<uint32_t>(u >> 32))) << 32 |
+                                        dpp<CTRL, ROWS>(static_cast<uint32_t>(u)));
 }
-constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;   // within a row: after all four, of 16 lanes
+constexpr int kNextRow = 0x142, kUpperRows = 0x143;   // a row's last lane to the next row (rows 1, 3), lane 31's to rows 2, 3
 
 __device__ __forceinline__ double lane_d(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -61,9 +70,9 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = max(v, dpp<kXor2>(v));
   v = max(v, dpp<kHalfMirror>(v));
   v = max(v, dpp<kMirror>(v));
-  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
-  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-  return max(max(a, b), max(c, d));
+  v = max(v, dpp<kNextRow, 0xa>(v));
+  v = max(v, dpp<kUpperRows, 0xc>(v));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
 }
 __device__ __forceinline__ float wave_max_f(float v) {
   // non-NaN floats order as their mapped bits
@@ -76,18 +85,24 @@ __device__ __forceinline__ double wave_sum_d(double v) {
   v += dpp<kXor2>(v);
   v += dpp<kHalfMirror>(v);
   v += dpp<kMirror>(v);
-  return (lane_d(v, 0) + lane_d(v, 16)) + (lane_d(v, 32) + lane_d(v, 48));
+  v += dpp<kNextRow, 0xa>(v);
+  v += dpp<kUpperRows, 0xc>(v);
+  return lane_d(v, 63);
 }
 
-// The two largest of two ordered pairs.
+// The two largest of an ordered pair and a value, and of two ordered pairs.
+__device__ __forceinline__ void push2(double& v1, double& v2, double o) {
+  v2 = fmax(v2, fmin(v1, o));
+  v1 = fmax(v1, o);
+}
 __device__ __forceinline__ void merge2(double& v1, double& v2, double o1, double o2) {
   v2 = fmax(fmin(v1, o1), fmax(v2, o2));
   v1 = fmax(v1, o1);
 }
 
-// KS: slots per lane for the chosen (k <= 64 * KS).
-template <int P, bool BF16, int KS>
-__global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const void* __restrict__ logits,
+// Eight wavefronts a SIMD up to P = 4 (its 8192 tokens run at once), registers permitting above.
+template <int P, bool BF16>
+__global__ __launch_bounds__(kWave * kWavesPerBlock, P <= 4 ? 8 : P <= 6 ? 6 : 5) void route_kernel(const void* __restrict__ logits,
                                                                        const float* __restrict__ bias, RouteArgs a) {
   __shared__ double vals[kWavesPerBlock][P * kWave];   // group values by way of LDS (group_lanes == 0)
   const int w = threadIdx.x >> 6, lane = lane_id();
@@ -112,7 +127,7 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const voi
       if constexpr (BF16) l[i] = bf16_to_f32(v[i]);
       else l[i] = v[i];
     }
-  } else {
+  } else if (e0 < E) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (e0 + i >= E) continue;
@@ -143,14 +158,18 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const voi
       sum += s[i];
     }
     sum = wave_sum_d(sum);
+    const double share = sum > 0.0 ? 1.0 / sum : 0.0;        // the sum is at least 1 or 0
 #pragma unroll
-    for (int i = 0; i < P; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+    for (int i = 0; i < P; ++i) s[i] *= share;
   }
 
-  uint64_t key[P];
+  uint32_t hi[P], lo[P];                        // choice values' keys
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    key[i] = e0 + i < E ? key_of(bias ? s[i] + static_cast<double>(b[i]) : static_cast<double>(l[i])) : 0ull;
+  for (int i = 0; i < P; ++i) {
+    const uint64_t key = key_of(bias ? s[i] + static_cast<double>(b[i]) : static_cast<double>(l[i]));
+    hi[i] = e0 + i < E ? static_cast<uint32_t>(key >> 32) : 0u;
+    lo[i] = static_cast<uint32_t>(key);
+  }
 
   if (a.n_groups > 1) {
     // what a group is valued by: choice values (NaN as -inf), or scores
@@ -164,15 +183,23 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const voi
     const bool two = a.top2 && size > 1;
     double v1 = -__builtin_inf(), v2 = -__builtin_inf();
     const int L = a.group_lanes;
-    if (L > 0) {
+    if (L > 0 && two) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) merge2(v1, v2, g[i], -__builtin_inf());
+      for (int i = 0; i < P; ++i) push2(v1, v2, g[i]);
       // after each step every lane of the doubled run holds the run's two largest
       if (L > 1) merge2(v1, v2, dpp<kXor1>(v1), dpp<kXor1>(v2));
       if (L > 2) merge2(v1, v2, dpp<kXor2>(v1), dpp<kXor2>(v2));
       if (L > 4) merge2(v1, v2, dpp<kHalfMirror>(v1), dpp<kHalfMirror>(v2));
       if (L > 8) merge2(v1, v2, dpp<kMirror>(v1), dpp<kMirror>(v2));
       if (L > 16) merge2(v1, v2, __shfl_xor(v1, 16, kWave), __shfl_xor(v2, 16, kWave));
+    } else if (L > 0) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v1 = fmax(v1, g[i]);
+      if (L > 1) v1 = fmax(v1, dpp<kXor1>(v1));
+      if (L > 2) v1 = fmax(v1, dpp<kXor2>(v1));
+      if (L > 4) v1 = fmax(v1, dpp<kHalfMirror>(v1));
+      if (L > 8) v1 = fmax(v1, dpp<kMirror>(v1));
+      if (L > 16) v1 = fmax(v1, __shfl_xor(v1, 16, kWave));
     } else {
 #pragma unroll
       for (int i = 0; i < P; ++i) vals[w][e0 + i] = g[i];
@@ -180,7 +207,7 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const voi
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       if (lane < a.n_groups)
-        for (int j = 0; j < size; ++j) merge2(v1, v2, vals[w][lane * size + j], -__builtin_inf());
+        for (int j = 0; j < size; ++j) push2(v1, v2, vals[w][lane * size + j]);
     }
     double v = two ? v1 + v2 : v1;
     if (v != v) v = -__builtin_inf();
@@ -195,39 +222,44 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const voi
     const bool stays = rank < a.top_groups;
     if (L > 0) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) key[i] = stays ? key[i] : 0ull;
+      for (int i = 0; i < P; ++i) hi[i] = stays ? hi[i] : 0u;
     } else {
       const uint64_t kept = __ballot(stays && lane < a.n_groups);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         const int gi = (e0 + i) / size;
-        if (gi >= a.n_groups || !((kept >> gi) & 1)) key[i] = 0ull;
+        if (gi >= a.n_groups || !((kept >> gi) & 1)) hi[i] = 0u;
       }
     }
   }
 
-  // k rounds: the largest key, the lowest expert that has it.  Round r is kept by lane r % 64,
-  // slot r / 64.  A retired key's upper half is 0, which no other key's is.
-  uint32_t hi[P], lo[P];
+  // k rounds: the largest key, the lowest expert that has it.  The expert chosen in round r
+  // keeps r + 1 in place of its key's upper half (k <= 512, below kNoKey).  One expert nearly
+  // always has the largest upper half alone; then its mask is all that the round needs.
+  bool twice = false;                           // two experts of a lane share an upper half
 #pragma unroll
-  for (int i = 0; i < P; ++i) hi[i] = static_cast<uint32_t>(key[i] >> 32), lo[i] = static_cast<uint32_t>(key[i]);
-  int cid[KS];
+  for (int i = 1; i < P; ++i)
 #pragma unroll
-  for (int i = 0; i < KS; ++i) cid[i] = 0;
-  for (int r = 0; r < a.k; ++r) {
+    for (int j = 0; j < i; ++j) twice |= hi[i] == hi[j] && hi[i] > kNoKey;
+  const bool pairs = __builtin_amdgcn_readfirstlane(__any(twice));
+  for (int r = 1; r <= a.k; ++r) {
     uint32_t best = hi[0];
 #pragma unroll
     for (int i = 1; i < P; ++i) best = max(best, hi[i]);
     const uint32_t top = wave_max_u32(best);
     uint64_t m[P], any = 0;
-    int n = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       m[i] = __ballot(hi[i] == top);
       any |= m[i];
-      n += __popcll(m[i]);
     }
-    if (n > 1) {                                // several share the upper half: the lower ones tell
+    int n = __popcll(any);
+    if (pairs) {
+      n = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) n += __popcll(m[i]);
+    }
+    if (n > 1) {                                // the lower halves tell, then the lowest lane and its lowest slot
       uint32_t b = 0;
 #pragma unroll
       for (int i = 0; i < P; ++i) b = max(b, hi[i] == top ? lo[i] : 0u);
@@ -238,58 +270,40 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock) void route_kernel(const voi
         m[i] = __ballot(hi[i] == top && lo[i] == low);
         any |= m[i];
       }
+      uint64_t left = any & -any;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        m[i] &= left;
+        left &= ~m[i];
+      }
     }
-    const int wl = __ffsll(static_cast<unsigned long long>(any)) - 1;   // the lowest lane, its lowest slot
-    int ws = P - 1;
 #pragma unroll
-    for (int i = P - 2; i >= 0; --i) ws = (m[i] >> wl) & 1 ? i : ws;
-    const bool mine = lane == wl;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (ws == i) hi[i] = mine ? 0u : hi[i];   // ws is wave-uniform
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-      if (KS == 1 || r / kWave == i) cid[i] = lane == r % kWave ? wl * P + ws : cid[i];
+    for (int i = 0; i < P; ++i) hi[i] = __builtin_amdgcn_inverse_ballot_w64(m[i]) ? static_cast<uint32_t>(r) : hi[i];
   }
-  // the chosen experts' scores, from the lanes that hold them
-  double cs[KS], sum = 0.0;
+  double sum = 0.0;
 #pragma unroll
-  for (int j = 0; j < KS; ++j) {
-    const int from = cid[j] / P, slot = cid[j] - from * P;
-    cs[j] = 0.0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const double v = __shfl(s[i], from, kWave);
-      cs[j] = slot == i ? v : cs[j];
-    }
-    if (j * kWave + lane >= a.k) cs[j] = 0.0;
-    sum += cs[j];
-  }
+  for (int i = 0; i < P; ++i) sum += hi[i] - 1u < static_cast<uint32_t>(a.k) ? s[i] : 0.0;
   const double denom = a.renormalize ? wave_sum_d(sum) : 1.0;
   const double factor = denom > 0.0 ? static_cast<double>(a.scale) / denom : 0.0;
+  // each lane writes its chosen experts at their places
+  const size_t at = static_cast<size_t>(t) * a.k;
 #pragma unroll
-  for (int j = 0; j < KS; ++j) {
-    const int at = j * kWave + lane;
-    if (at < a.k) {
-      a.topk_ids[static_cast<size_t>(t) * a.k + at] = cid[j];
-      a.topk_w[static_cast<size_t>(t) * a.k + at] = static_cast<float>(cs[j] * factor);
+  for (int i = 0; i < P; ++i) {
+    const uint32_t r = hi[i] - 1u;
+    if (r < static_cast<uint32_t>(a.k)) {
+      a.topk_ids[at + r] = e0 + i;
+      a.topk_w[at + r] = static_cast<float>(s[i] * factor);
     }
   }
-}
-
-template <int P, int KS>
-void launch_k(const void* logits, const float* bias, const RouteArgs& a, hipStream_t stream) {
-  dim3 grid((a.T + kWavesPerBlock - 1) / kWavesPerBlock), block(kWave * kWavesPerBlock);
-  if (a.bf16)
-    hipLaunchKernelGGL((route_kernel<P, true, KS>), grid, block, 0, stream, logits, bias, a);
-  else
-    hipLaunchKernelGGL((route_kernel<P, false, KS>), grid, block, 0, stream, logits, bias, a);
 }
 
 template <int P>
 void launch_p(const void* logits, const float* bias, const RouteArgs& a, hipStream_t stream) {
-  if (a.k <= kWave) launch_k<P, 1>(logits, bias, a, stream);
-  else launch_k<P, P>(logits, bias, a, stream);   // k <= E <= 64 * P
+  dim3 grid((a.T + kWavesPerBlock - 1) / kWavesPerBlock), block(kWave * kWavesPerBlock);
+  if (a.bf16)
+    hipLaunchKernelGGL((route_kernel<P, true>), grid, block, 0, stream, logits, bias, a);
+  else
+    hipLaunchKernelGGL((route_kernel<P, false>), grid, block, 0, stream, logits, bias, a);
 }
 
 }  // namespace
