@@ -126,49 +126,54 @@ constexpr int kWavesS = kThreadsS / kWave;
 constexpr int kChunk = 512;
 constexpr int kPitch = kChunk + 16;  // bytes of a staged row: 16 rows start in 16 different bank groups
 
-// The block's item, found from the group offsets (every thread calls it).
-__device__ Item find_item(const ProductArgs& p, int BM, int nch) {
-  constexpr int GPT = (kMaxGroups + kThreadsS - 1) / kThreadsS;
-  __shared__ int wsum[kWavesS];
-  __shared__ Item found;
-  const int tid = threadIdx.x, lane = lane_id(), w = tid >> 6;
-  const int x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-  if (tid == 0) found = Item{0, 0, 0, 0, 0, 0};
-  GroupRows gr[GPT];
-  int s = 0;
-#pragma unroll
-  for (int q = 0; q < GPT; ++q) {
-    const int g = tid * GPT + q;
-    gr[q] = GroupRows{0, 0, 0, 0, 0, 0};
-    if (g < p.G) {
-      gr[q] = group_rows(p.offs, p.n_rows, p.E, p.nseg, BM, g);
-      s += group_items(gr[q], g, nch, x);
-    }
-  }
-  int incl = s;
+// Sum of v over the lanes up to this one.
+__device__ __forceinline__ int wave_prefix(int v) {
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
-    const int y = __shfl_up(incl, o, kWave);
-    if (lane >= o) incl += y;
+    const int y = __shfl_up(v, o, kWave);
+    if (lane_id() >= o) v += y;
   }
-  if (lane == kWave - 1) wsum[w] = incl;
-  __syncthreads();
-  int base = 0;
-#pragma unroll
-  for (int i = 0; i < kWavesS; ++i) base += i < w ? wsum[i] : 0;
-  int t = base + incl - s;
-  if (slot >= t && slot < t + s) {
-#pragma unroll
-    for (int q = 0; q < GPT; ++q) {
-      const int g = tid * GPT + q;
-      if (g >= p.G) break;
-      const int n = group_items(gr[q], g, nch, x);
-      if (slot >= t && slot < t + n) found = group_item(gr[q], g, nch, x, slot - t, BM, p.E, p.nseg);
-      t += n;
+  return v;
+}
+
+// The block's item, found from the group offsets.  Every wave finds it by itself, so that
+// nothing waits for another: a lane counts the items of `per` neighbouring groups, a sum
+// over the lanes tells whose the block's is, and where per > 1 the lanes then take that
+// lane's groups one each.  The result is wave-uniform, in scalar registers.
+__device__ Item find_item(const ProductArgs& p, int BM, int nch) {
+  const int lane = lane_id(), x = blockIdx.x % kXcds;
+  const int per = (p.G + kWave - 1) / kWave;                // <= 64: at most 1280 groups
+  int slot = blockIdx.x / kXcds;
+  GroupRows r{0, 0, 0, 0, 0, 0};
+  int n = 0, g0 = 0;
+  for (int i = 0; i < per; ++i) {
+    const int g = lane * per + i;
+    if (g < p.G) {
+      r = group_rows(p.offs, p.n_rows, p.E, p.nseg, BM, g);
+      n += group_items(r, g, nch, x);
     }
   }
-  __syncthreads();
-  return found;
+  int at = wave_prefix(n) - n;
+  uint64_t here = __ballot(slot >= at && slot < at + n);
+  if (here == 0) return Item{0, 0, 0, 0, 0, 0};
+  int w = __builtin_ctzll(here);
+  slot -= __builtin_amdgcn_readlane(at, w);
+  if (per > 1) {
+    g0 = w * per;
+    n = 0;
+    if (lane < per && g0 + lane < p.G) {
+      r = group_rows(p.offs, p.n_rows, p.E, p.nseg, BM, g0 + lane);
+      n = group_items(r, g0 + lane, nch, x);
+    }
+    at = wave_prefix(n) - n;
+    here = __ballot(slot >= at && slot < at + n);
+    w = __builtin_ctzll(here);
+    slot -= __builtin_amdgcn_readlane(at, w);
+  }
+  const GroupRows u{__builtin_amdgcn_readlane(r.a0, w), __builtin_amdgcn_readlane(r.na, w),
+                    __builtin_amdgcn_readlane(r.b0, w), __builtin_amdgcn_readlane(r.nb, w),
+                    __builtin_amdgcn_readlane(r.t0, w), __builtin_amdgcn_readlane(r.nt, w)};
+  return group_item(u, g0 + w, nch, x, slot, BM, p.E, p.nseg);
 }
 
 template <int MF, Mode M, class Out>
