@@ -63,6 +63,11 @@ def _ok(t: torch.Tensor, index: int, dtype, shape) -> bool:
     return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
 
 
+def _new(rows: int, cols: int, dtype, index: int) -> torch.Tensor:
+    """torch.empty((rows, cols)) on GPU `index`, in three quarters of its time."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=index)
+
+
 def _call(name: str, index: int, fn, *args) -> None:
     """fn(*args, stream) on GPU `index` and its current stream."""
     if torch._C._cuda_getDevice() == index:
@@ -157,17 +162,19 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[t
         raise ValueError(f"score must be one of {sorted(_lib.SCORES)}")
     if group_rank not in _lib.GROUP_RANKS:
         raise ValueError(f"group_rank must be one of {sorted(_lib.GROUP_RANKS)}")
+    if bias is not None and not _ok(bias, index, torch.float32, (E,)):
+        _out(bias, "bias", torch.float32, (E,))
+        _same_device(logits, bias=bias)
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    if not ((bias is None or _ok(bias, index, torch.float32, (E,))) and _ok(topk_ids, index, torch.int32, (T, k)) and
-            _ok(topk_w, index, torch.float32, (T, k))):
-        if bias is not None:
-            _out(bias, "bias", torch.float32, (E,))
+        topk_ids = _new(T, k, torch.int32, index)
+    elif not _ok(topk_ids, index, torch.int32, (T, k)):
         _out(topk_ids, "topk_ids", torch.int32, (T, k))
+        _same_device(logits, topk_ids=topk_ids)
+    if topk_w is None:
+        topk_w = _new(T, k, torch.float32, index)
+    elif not _ok(topk_w, index, torch.float32, (T, k)):
         _out(topk_w, "topk_w", torch.float32, (T, k))
-        _same_device(logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
+        _same_device(logits, topk_w=topk_w)
     _call("moe_route", index, _lib.load().moe_route, logits.data_ptr(), _dtype_code(logits), _ptr(bias), T, E, k,
           _lib.SCORES[score], n_groups, n_groups if top_groups is None else top_groups, _lib.GROUP_RANKS[group_rank],
           1 if renormalize else 0, scale, topk_ids.data_ptr(), topk_w.data_ptr())
@@ -538,17 +545,21 @@ def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optio
     _need(x, "x")
     if x.dim() < 1:
         raise ValueError("x must have at least one dim")
-    if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    if s is None:
-        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     index = x.get_device()
-    if not (_ok(q, index, torch.int8, x.shape) and _ok(s, index, torch.float32, x.shape[:-1])):
-        _out(q, "q", torch.int8, x.shape)
-        _out(s, "s", torch.float32, x.shape[:-1])
-        _same_device(x, q=q, s=s)
+    *rows, d = shape = x.shape
+    if q is None:
+        q = _new(*rows, d, torch.int8, index) if len(rows) == 1 else torch.empty(shape, dtype=torch.int8, device=index)
+    elif not _ok(q, index, torch.int8, shape):
+        _out(q, "q", torch.int8, shape)
+        _same_device(x, q=q)
+    if s is None:
+        s = torch.empty_strided(rows, (1,), dtype=torch.float32, device=index) if len(rows) == 1 else \
+            torch.empty(rows, dtype=torch.float32, device=index)
+    elif not _ok(s, index, torch.float32, shape[:-1]):
+        _out(s, "s", torch.float32, shape[:-1])
+        _same_device(x, s=s)
     _call("moe_quantize_rows_i8", index, _lib.load().moe_quantize_rows_i8, x.data_ptr(), _dtype_code(x), s.numel(),
-          x.shape[-1], q.data_ptr(), s.data_ptr())
+          d, q.data_ptr(), s.data_ptr())
     return q, s
 
 
@@ -584,20 +595,23 @@ def grouped_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, group_offsets: to
     out (y's dtype, or `out_dtype`).  E = 1 with offsets [0, N] is a plain
     linear map (moe_grouped_linear_i8)."""
     _need(xq, "xq", torch.int8, 2)
-    _need(w, "w", torch.int8, 3)
+    if w.dim() != 3:
+        _need(w, "w", torch.int8, 3)
     n_x, K = xq.shape
-    G, O = E + n_shared, w.shape[1]
+    G, O = E + n_shared, w.size(1)
     index = xq.get_device()
     N = _i8_batch(xq, x_rows, group_offsets, E, n_shared, nseg)
-    if y is None:
-        y = torch.empty((N, O), dtype=out_dtype, device=xq.device)
     if not (_ok(x_scale, index, torch.float32, (n_x,)) and _ok(w, index, torch.int8, (G, O, K)) and
-            _ok(w_scale, index, torch.float32, (G, O)) and _ok(y, index, y.dtype, (N, O))):
+            _ok(w_scale, index, torch.float32, (G, O))):
         _out(x_scale, "x_scale", torch.float32, (n_x,))
         _out(w, "w", torch.int8, (G, O, K))
         _out(w_scale, "w_scale", torch.float32, (G, O))
+        _same_device(xq, x_scale=x_scale, w=w, w_scale=w_scale)
+    if y is None:
+        y = _new(N, O, out_dtype, index)
+    elif not _ok(y, index, y.dtype, (N, O)):
         _out(y, "y", y.dtype, (N, O))
-        _same_device(xq, x_scale=x_scale, w=w, w_scale=w_scale, y=y)
+        _same_device(xq, y=y)
     _call("moe_grouped_linear_i8", index, _lib.load().moe_grouped_linear_i8, xq.data_ptr(), x_scale.data_ptr(),
           _ptr(x_rows), n_x, group_offsets.data_ptr(), N, E, n_shared, nseg, K, O, w.data_ptr(), w_scale.data_ptr(),
           _dtype_code(y), y.data_ptr())
@@ -642,16 +656,18 @@ def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_share
     I, G = w_gate.shape[1], E + n_shared
     index = x.get_device()
     N = _i8_batch(x, x_rows, group_offsets, E, n_shared, nseg)
+    _need_i8_weights(x, G, d, I, (w_gate, s_gate, w_up, s_up, w_down, s_down))
     if h_sorted is None:
-        h_sorted = torch.empty((N, d), dtype=torch.bfloat16, device=x.device)
+        h_sorted = _new(N, d, torch.bfloat16, index)
+    elif not _ok(h_sorted, index, torch.bfloat16, (N, d)):
+        _out(h_sorted, "h_sorted", torch.bfloat16, (N, d))
+        _same_device(x, h_sorted=h_sorted)
     if workspace is None:
         workspace = torch.empty(max(ffn_i8_workspace_bytes(N, n_x, d, I, E, n_shared, nseg), 256), dtype=torch.uint8,
-                                device=x.device)
-    _need_i8_weights(x, G, d, I, (w_gate, s_gate, w_up, s_up, w_down, s_down))
-    if not (_ok(h_sorted, index, torch.bfloat16, (N, d)) and _ok(workspace, index, torch.uint8, (workspace.numel(),))):
-        _out(h_sorted, "h_sorted", torch.bfloat16, (N, d))
+                                device=index)
+    elif not _ok(workspace, index, torch.uint8, (workspace.numel(),)):
         _out(workspace, "workspace", torch.uint8, (workspace.numel(),))
-        _same_device(x, h_sorted=h_sorted, workspace=workspace)
+        _same_device(x, workspace=workspace)
     nbytes = ctypes.c_size_t(workspace.numel())
     _call("moe_grouped_ffn_i8", index, _lib.load().moe_grouped_ffn_i8, x.data_ptr(), _ptr(x_rows), n_x,
           group_offsets.data_ptr(), N, E, n_shared, nseg, d, I, w_gate.data_ptr(), s_gate.data_ptr(), w_up.data_ptr(),
