@@ -392,29 +392,58 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs
   const int run = ((K + kBlock - 1) / kBlock + kSplit - 1) / kSplit * kBlock;
   const int k0 = min(K, wave * run), k1 = min(K, k0 + run);
   const size_t rb = static_cast<size_t>(it.expert) * cols + it.chunk * 16 * NC;
-  const int8_t* wp[NF];
+  const int8_t* wp[NF];                                     // wave-uniform; a lane's 16 bytes are its `lane`-th
 #pragma unroll
-  for (int j = 0; j < NF; ++j) wp[j] = (j < NC ? p.w0 : p.w1) + (rb + 16 * (j % NC)) * K + lane * 16;
+  for (int j = 0; j < NF; ++j) wp[j] = (j < NC ? p.w0 : p.w1) + (rb + 16 * (j % NC)) * K;
   uint4 w[U][NF];
-  auto load_w = [&](int k) MOE_INLINE {
+  // Loads without branches, so that the waits count them one by one: a step past this wave's
+  // run loads the matrix's last one (where K is short), which is not multiplied.
+  auto step_at = [&](int k, int u) MOE_INLINE { return static_cast<size_t>(min(k + u * kStep, K - kStep)); };
+  auto load_w = [&](int k, int u0, int u1) MOE_INLINE {
+#pragma unroll
+    for (int u = u0; u < u1; ++u)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) w[u][j] = reinterpret_cast<const uint4*>(wp[j] + step_at(k, u) * 16)[lane];
+  };
+  // this lane's row (lanes past the rows repeat the last one) and its 16 values of each K step: bf16, fp32 or codes
+  const int row = it.row(min(l16, it.rows - 1));
+  constexpr int PIECES = M == kGateUp ? 2 : M == kDown ? 4 : 1;
+  uint4 x[U][PIECES];
+  const uint8_t* xr = nullptr;
+  auto load_x = [&](int k) MOE_INLINE {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < NF; ++j)
-        w[u][j] = k + u * kStep < k1 ? *reinterpret_cast<const uint4*>(wp[j] + static_cast<size_t>(k + u * kStep) * 16)
-                                     : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < PIECES; ++i) x[u][i] = reinterpret_cast<const uint4*>(xr + step_at(k, u) * PIECES)[i];
   };
-  load_w(k0);
-  const int row = it.row(min(l16, it.rows - 1));            // lanes past the rows repeat the last one
-  const int src = M == kDown ? row : src_row(p, row);
+  // A wave's loads return in order, so the first rows are asked for among the first weights: behind them
+  // (17.8 us for one token's FFN) what the rows are still to go through would wait for every weight.
+  int src = row;
+  if constexpr (M == kDown) {
+    xr = reinterpret_cast<const uint8_t*>(p.af + static_cast<size_t>(row) * K + 16 * q);
+    load_x(k0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(k0, 0, U);
+  } else {
+    const int listed = *(p.x_rows ? p.x_rows + row : p.offs);
+    load_w(k0, 0, U / 2);
+    __builtin_amdgcn_sched_barrier(0);
+    if (p.x_rows) src = min(max(listed, 0), p.n_x - 1);
+    const uint8_t* base = static_cast<const uint8_t*>(M == kGateUp ? p.x : p.a);
+    xr = base + (static_cast<size_t>(src) * K + 16 * q) * (M == kGateUp ? 2 : 1);
+    load_x(k0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(k0, U / 2, U);
+  }
+  __builtin_amdgcn_sched_barrier(0);
 
   QuantScale qs{1.f, 1.f, 1.f, 1.f};                        // kGateUp: of this lane's token
-  const uint16_t* xr = nullptr;
   if constexpr (M == kGateUp) {
-    xr = static_cast<const uint16_t*>(p.x) + static_cast<size_t>(src) * K + 16 * q;
     uint32_t m = 0;
-    for (int k = k0; k < k1; k += kStep) {
-      const uint4* v = reinterpret_cast<const uint4*>(xr + k);
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = max(m, max(bf16_max(x[u][0]), bf16_max(x[u][1])));   // repeated steps change nothing
+    for (int k = k0 + U * kStep; k < k1; k += kStep) {
+      const uint4* v = reinterpret_cast<const uint4*>(xr + static_cast<size_t>(k) * 2);
       m = max(m, max(bf16_max(v[0]), bf16_max(v[1])));
     }
     m = max_over_q(m);
@@ -431,20 +460,21 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs
 #pragma unroll
   for (int j = 0; j < NF; ++j) acc[j] = i32x4{0, 0, 0, 0};
   for (int k = k0; k < k1; k += U * kStep) {
-    if (k != k0) load_w(k);
+    if (k != k0) {
+      load_x(k);
+      load_w(k, 0, U);
+    }
     if constexpr (M == kDown) {
-      // blocks of 128 columns of the fp32 product: their scale, then their codes
+      // blocks of 128 columns of the fp32 product: their scale, then their codes (columns past K are zeros)
 #pragma unroll
       for (int u = 0; u < U; u += 2) {
-        const int kb = k + u * kStep;
-        if (kb >= k1) break;
-        const bool two = kb + kStep < k1;
-        const float* ar = p.af + static_cast<size_t>(row) * K + kb + 16 * q;
+        if (k + u * kStep >= k1) break;
         float v[8][4];
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const f32x4 f = i < 4 || two ? *reinterpret_cast<const f32x4*>(ar + (i / 4) * kStep + 4 * (i % 4)) : f32x4{0.f, 0.f, 0.f, 0.f};
+          f32x4 f = __builtin_bit_cast(f32x4, x[u + i / 4][i % 4]);
+          if (i >= 4 && k + (u + 1) * kStep >= k1) f = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             v[i][r] = f[r];
@@ -466,15 +496,9 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int ku = k + u * kStep;
-        if (ku >= k1) break;
-        uint4 a;
-        if constexpr (M == kGateUp) {
-          const uint4* v = reinterpret_cast<const uint4*>(xr + ku);
-          a = bf16_codes(v[0], v[1], qs);
-        } else {
-          a = *reinterpret_cast<const uint4*>(p.a + static_cast<size_t>(src) * K + ku + 16 * q);
-        }
+        if (k + u * kStep >= k1) break;
+        uint4 a = x[u][0];
+        if constexpr (M == kGateUp) a = bf16_codes(x[u][0], x[u][1], qs);
 #pragma unroll
         for (int j = 0; j < NF; ++j) acc[j] = mfma_i8(w[u][j], a, acc[j]);
       }
