@@ -121,6 +121,11 @@ __device__ __forceinline__ void store4(Out* p, const float (&v)[4]) {
 // columns): each wave owns 16 columns (kGateUp: 16 gate rows and 16 up rows) and
 // reads their weights once; the rows' codes are staged through LDS, 512 of K at a
 // time, double buffered, and shared by the waves.
+// Bound by the weights' bytes: 128 tokens x 8 of 64 experts, 2048 -> 1024, 137 MB in 30 us
+// (4.6 TB/s); an FFN of 1088 tokens x 4 of 128 experts, 2880 x 2880, whose used experts'
+// weights are 2.7 GB, 551 us (4.95 TB/s, the rate of a copy).  Asking for a step's next
+// weights as soon as it is multiplied, instead of a chunk's together, changes 1 % either
+// way; loads without the branches of a chunk past K are 2 % slower.
 constexpr int kThreadsS = 512;
 constexpr int kWavesS = kThreadsS / kWave;
 constexpr int kChunk = 512;
@@ -341,6 +346,8 @@ __global__ __launch_bounds__(kThreadsS, MF == 4 ? 2 : 4) void stream_i8(ProductA
 // to draw the weights through every CU, so an item is 16 columns (kGateUp: 16 gate and 16
 // up rows) of at most 16 rows and the eight waves split K; their sums are joined through
 // LDS.  A wave's first weights are requested before anything else happens.
+// Bound by that chain (group offsets, weights, rows, join) around one burst of weights: one
+// token's FFN, 8 experts of 2048 x 1024 (50 MB), 16.6 us; 5 rows x 2048 -> 2048 (4 MB) 3.9.
 // The FFN's quantisations move to where codes are used, because a block no longer holds
 // the columns that share a scale, and each block repeats them (16 rows at most):
 //   * kGateUp reads the bf16 tokens: a wave's slice of K gives part of a row's largest
@@ -555,6 +562,14 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs
 //     compiler sees would make it wait for everything in flight.
 // Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave,
 // so the rows of a partial tile spread over them.
+// 8191 x 2048 -> 4096 (fp32 out) takes 79 us, 1.74 POP/s; K = 8192 reaches 2.5.  The matrix
+// cores are busy 43 % of the cycles, waves wait 41 %: the barrier of each 64-wide step, the
+// first loads and the epilogue of a tile (some 7 us of 35) bound it.  An FFN of 4096 tokens x 8
+// of 128 experts, 2048 x 768, 266 us: a fifth of it are the experts' weights coming from HBM
+// (every tile on one expert's: 0.83 of the time), the rest ragged tiles and, in kDown, the
+// conversion and fma for each product.  Not kept: waves of 128 x 128, sixteen waves, panels of
+// 2 or 8 column chunks, tiles of equal height within a group, skipping the operand reads of
+// empty blocks (each within 2 % or slower).
 template <int MI_, int NJ_, int WM_, int WN_, int BPC_>
 struct TileCfg {
   static constexpr int BPC = BPC_;                             // blocks per CU
@@ -1037,18 +1052,19 @@ using TileDown = TileWide;
 
 // Which kernel: the host sees the average group, not the groups.  Times of the whole call,
 // us; d, I or K, O = 2048, 1024 (FFN, 64 groups) and 2048, 2048 (linear, one group).
-//   few_i8 or stream_i8     linear 128 rows 6.9 / 11.6, 256 rows 11.3 / 11.7: few_i8 up to
-//                           kFewBlocksMost items of 16 x 16.  FFN of one token (8 rows)
-//                           19 / 20; 16 groups of one row, 1024 x 512, 12.7 / 14.6, of 8
-//                           rows 15.3 / 15.4; 64 groups of one row 137 / 80: only up to
+//   few_i8 or stream_i8     linear 16 rows 4.8 / 7.8, 128 rows 6.2 / 11.4, 512 rows 17.6 /
+//                           12.1: few_i8 up to kFewBlocksMost items of 16 x 16 (1024 x 512,
+//                           twice as many: 9.3 / 8.6).  FFN with 8 groups of one row 16.5 /
+//                           18.6, of 8 rows 23.1 / 19.3; 16 groups of one row, 1024 x 512,
+//                           11.7 / 13.3; 64 groups of one row 106 / 75: only up to
 //                           kFewItems items of 128 columns, which also bounds the fp32
 //                           product to 80 KiB.
-//   stream_i8 or tile_i8    64 rows a group 124 / 118, 96 rows 167 / 127; but linear 2048
-//                           rows (512 items of 64 x 128) 20 / 24, 4096 rows 40 / 30, 16
-//                           groups of 256 rows, 1024 x 512 (256 items) 37 / 44: tile_i8
+//   stream_i8 or tile_i8    64 rows a group 114 / 113, 96 rows 151 / 117; but linear 2048
+//                           rows (512 items of 64 x 128) 20 / 24, 4096 rows 38 / 32, 16
+//                           groups of 256 rows, 1024 x 512 (256 items) 34 / 44: tile_i8
 //                           needs both full tiles and enough of them.
-//   TileHalf or TileWide    128 rows a group 136 / 142, 192 rows 163 / 158; linear 4096 rows
-//                           (128 wide tiles) 30 / 34, 8191 x 4096 (512) 85 / 79.
+//   TileHalf or TileWide    128 rows a group 125 / 130, 192 rows 156 / 147; linear 4096 rows
+//                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
 constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
 constexpr int kTileMinAvg = 48, kTileMinItems = 640;
 constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
