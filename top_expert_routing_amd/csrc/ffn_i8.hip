@@ -3,7 +3,7 @@
 //
 // Rows are int8 codes with one scale per row, expert matrices packed int8 codes
 // with one scale per output channel; the sums are exact int32 and the scales
-// multiply them in fp32.  Three kinds of products share two kernels:
+// multiply them in fp32.  Three kinds of products share three kernels (few_i8, stream_i8, tile_i8):
 //   kLinear  y = sx * sw * (xq . W)                                     -> bf16 or fp32
 //   kGateUp  a = silu(sx sg (xq . Wg)) * (sx su (xq . Wu)), quantised per row and
 //            128 columns (the columns of one tile)                      -> codes + scales
