@@ -1061,13 +1061,17 @@ using TileDown = TileWide;
 //                           kFewItems items of 128 columns, which also bounds the fp32
 //                           product to 80 KiB.
 //   stream_i8 or tile_i8    64 rows a group 114 / 113, 96 rows 151 / 117; but linear 2048
-//                           rows (512 items of 64 x 128) 20 / 24, 4096 rows 38 / 32, 16
-//                           groups of 256 rows, 1024 x 512 (256 items) 34 / 44: tile_i8
-//                           needs both full tiles and enough of them.
+//                           rows (512 items of 64 x 128) 20 / 24, 5800 rows x 2112 -> 832
+//                           (589) 33 / 30, 4096 rows (1024) 38 / 32, 16 groups of 256
+//                           rows, 1024 x 512 (256 items) 34 / 44: tile_i8 needs both full
+//                           tiles and enough of them.  By the product of an FFN: gate/up 384 items 87 / 92, 528 items 93 / 87, 611 items 69 /
+//                           58; down 640 items 83 / 87, 700 items 71 / 76, 768 items 97 / 93,
+//                           917 items 82 / 69.
 //   TileHalf or TileWide    128 rows a group 125 / 130, 192 rows 156 / 147; linear 4096 rows
 //                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
 constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
-constexpr int kTileMinAvg = 48, kTileMinItems = 640;
+constexpr int kTileMinAvg = 48;
+constexpr int tile_min_items(Mode m) { return m == kGateUp ? 512 : m == kDown ? 736 : 576; }
 constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
 constexpr int kWideMinAvg = 192, kWideMinTiles = 256;
 
@@ -1104,7 +1108,7 @@ template <Mode M, class Out>
 void launch_product(const ProductArgs& p, hipStream_t stream) {
   const int avg = p.n_rows / p.G;
   const long long area = static_cast<long long>(p.n_rows) * p.cols;
-  if (avg > kTileMinAvg && p.K >= kTileMinK && area >= kTileMinItems * 64ll * 128) {
+  if (avg > kTileMinAvg && p.K >= kTileMinK && area >= tile_min_items(M) * 64ll * 128) {
     const long long wide = area / (256 * (M == kGateUp ? 128 : 256));
     // (the lists of two blocks per CU have room for some 380 groups)
     if (M == kDown || (avg >= kWideMinAvg && wide >= kWideMinTiles) ||
