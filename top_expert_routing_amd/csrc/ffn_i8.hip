@@ -1035,7 +1035,12 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Rows of stream_i8's tiles, 16 * mf: groups of the average size in one tile.
+// Rows of stream_i8's tiles, 16 * mf: groups of the average size in one tile.  Where that
+// leaves CUs without an item (at most kIdle... of them), half the rows: two items read the same
+// weights, one from the L2.  us without / with: linear 222 rows x 2048 -> 2048 11.7 / 7.2, 512
+// rows 11.8 / 8.8; FFN of 8 groups of 32 rows, 2048 x 1024, 26.9 / 20.3, 2 of 128 rows, 2048 x
+// 2048, 31.3 / 21.3.  At 200 or 256 items: linear 512 rows 8.8 / 10.0, FFN 16 groups of 64 rows,
+// 1024 x 512, 18.6 / 17.3.
 int pick_mf(int avg) { return avg <= 12 ? 1 : avg <= 28 ? 2 : 4; }
 
 // CUs of the current device.
@@ -1053,13 +1058,13 @@ using TileDown = TileWide;
 
 // Which kernel: the host sees the average group, not the groups.  Times of the whole call,
 // us; d, I or K, O = 2048, 1024 (FFN, 64 groups) and 2048, 2048 (linear, one group).
-//   few_i8 or stream_i8     linear 16 rows 4.8 / 7.8, 128 rows 6.2 / 11.4, 512 rows 17.6 /
-//                           12.1: few_i8 up to kFewBlocksMost items of 16 x 16 (1024 x 512,
-//                           twice as many: 9.3 / 8.6).  FFN with 8 groups of one row 16.5 /
-//                           18.6, of 8 rows 23.1 / 19.3; 16 groups of one row, 1024 x 512,
-//                           11.7 / 13.3; 64 groups of one row 106 / 75: only up to
-//                           kFewItems items of 128 columns, which also bounds the fp32
-//                           product to 80 KiB.
+//   few_i8 or stream_i8     linear 16 rows 4.8 / 6.7, 128 rows 6.1 / 6.8, 256 rows 9.9 /
+//                           7.2: few_i8 up to kFewBlocksMost items of 16 x 16 (1024 x 512,
+//                           512 rows 5.5 / 5.6, 1024 rows 9.2 / 7.1).  FFN with 8 groups of
+//                           one row 16.2 / 18.4, of 8 rows 23.8 / 19.2; 16 groups of one
+//                           row, 1024 x 512, 11.8 / 13.4; 64 groups of one row 106 / 75:
+//                           only up to kFewItems items of 128 columns, which also bounds the
+//                           fp32 product to 80 KiB.
 //   stream_i8 or tile_i8    64 rows a group 114 / 113, 96 rows 151 / 117; but linear 2048
 //                           rows (512 items of 64 x 128) 20 / 24, 5800 rows x 2112 -> 832
 //                           (589) 33 / 30, 4096 rows (1024) 38 / 32, 16 groups of 256
@@ -1070,6 +1075,7 @@ using TileDown = TileWide;
 //   TileHalf or TileWide    128 rows a group 125 / 130, 192 rows 156 / 147; linear 4096 rows
 //                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
 constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
+constexpr int kIdleLinear = 200, kIdleFfn = 256;
 constexpr int kTileMinAvg = 48;
 constexpr int tile_min_items(Mode m) { return m == kGateUp ? 512 : m == kDown ? 736 : 576; }
 constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
@@ -1119,8 +1125,10 @@ void launch_product(const ProductArgs& p, hipStream_t stream) {
     }
     return;
   }
-  const int mf = pick_mf(avg);
-  dim3 grid(item_grid(max_m_tiles(p, 16 * mf), (p.cols + kBlock - 1) / kBlock)), block(kThreadsS);
+  const int nch = (p.cols + kBlock - 1) / kBlock;
+  int mf = pick_mf(avg);
+  while (mf > 1 && max_m_tiles(p, 16 * mf) * nch <= (M == kLinear ? kIdleLinear : kIdleFfn)) mf /= 2;
+  dim3 grid(item_grid(max_m_tiles(p, 16 * mf), nch)), block(kThreadsS);
   switch (mf) {
     case 1: hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p); break;
     case 2: hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p); break;
