@@ -656,7 +656,10 @@ def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_share
     I, G = w_gate.shape[1], E + n_shared
     index = x.get_device()
     N = _i8_batch(x, x_rows, group_offsets, E, n_shared, nseg)
-    _need_i8_weights(x, G, d, I, (w_gate, s_gate, w_up, s_up, w_down, s_down))
+    i8, f32, ins, outs = torch.int8, torch.float32, (G, I), (G, d)
+    if not (_ok(w_gate, index, i8, (G, I, d)) and _ok(w_up, index, i8, (G, I, d)) and _ok(w_down, index, i8, (G, d, I)) and
+            _ok(s_gate, index, f32, ins) and _ok(s_up, index, f32, ins) and _ok(s_down, index, f32, outs)):
+        _need_i8_weights(x, G, d, I, (w_gate, s_gate, w_up, s_up, w_down, s_down))
     if h_sorted is None:
         h_sorted = _new(N, d, torch.bfloat16, index)
     elif not _ok(h_sorted, index, torch.bfloat16, (N, d)):
