@@ -579,3 +579,64 @@ def test_layer_refuses_what_its_raw_calls_would_read_wrongly():
     layer.int8_weights = good[:5] + (z(E, d - 1, dt=f),)
     with pytest.raises(ValueError):
         layer.bound_calls(z(T, E, dt=f), x)
+
+
+# groups of some 20 and 60 rows, enough of them that every CU has work at 32 and 64 rows a tile
+STREAM = {
+    "rows_32": dict(sizes=[14 + (5 * i) % 13 for i in range(64)], T=230, shared=1),
+    "rows_64": dict(sizes=[45 + (7 * i) % 31 for i in range(64)], T=150),
+    "rows_64_priority": dict(sizes=[40 + (7 * i) % 31 for i in range(48)], T=90, prio_sizes=[(11 * i) % 70 + 20 for i in range(48)]),
+}
+
+
+@pytest.mark.parametrize("name", STREAM)
+@pytest.mark.parametrize("K,O,dtype", [(192, 448, "f32"), (576, 384, "bf16")])
+def test_linear_many_small_groups(name, K, O, dtype):
+    announce(f"linear small groups {name} {K} {O} {dtype}")
+    g = _gen(K + O + len(name))
+    b = STREAM[name]
+    rows, offs, E, nseg = _batch(g, **b)
+    S = b.get("shared", 0)
+    xq, xs = _codes(g, b["T"], K), torch.rand(b["T"], generator=g) + 0.1
+    w, ws = _codes(g, E + S, O, K), torch.rand((E + S, O), generator=g) + 0.1
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    y = moe.grouped_linear_i8(xq.to(DEV), xs.to(DEV), offs.to(DEV), E, S, nseg, moe.pack_i8_codes(w).to(DEV), ws.to(DEV),
+                              x_rows=rows.to(DEV), out_dtype=dt)
+    torch.cuda.synchronize()
+    ref = Q.grouped_linear(xq.numpy(), xs.numpy(), rows.numpy(), offs.tolist(), E, nseg, w.numpy(), ws.numpy())
+    tol = (3 * 2.0 ** -24 + torch.finfo(dt).eps / 2) * (1 + 1e-6)
+    assert np.all(np.abs(f64_of(y) - ref) <= tol * np.abs(ref))
+
+
+@pytest.mark.parametrize("name", STREAM)
+def test_ffn_many_small_groups(name):
+    announce(f"ffn small groups {name}")
+    g = _gen(30 + len(name))
+    rows, offs, E, nseg, S, x, ws, ss = _ffn_case(g, STREAM[name], 448, 576)
+    h = moe.grouped_ffn_i8(x.to(DEV), offs.to(DEV), E, S, nseg, *_ffn_args(ws, ss), x_rows=rows.to(DEV))
+    torch.cuda.synchronize()
+    _ffn_check(f64_of(h), x, rows, offs, E, nseg, ws, ss)
+
+
+@pytest.mark.parametrize("rows,K,O", [(9, 8192, 64), (16, 2240, 192), (100, 64, 1024), (33, 1984, 512)])
+def test_linear_few_rows_long_and_short_sums(rows, K, O):
+    """K of one step, of fewer blocks than a block has waves, and of several batches per wave."""
+    announce(f"linear few rows {rows} {K} {O}")
+    g = _gen(rows + K)
+    xq, xs = _codes(g, rows, K), torch.rand(rows, generator=g) + 0.1
+    w, ws = _codes(g, 1, O, K), torch.rand((1, O), generator=g) + 0.1
+    offs = torch.tensor([0, rows], dtype=torch.int32)
+    y = moe.grouped_linear_i8(xq.to(DEV), xs.to(DEV), offs.to(DEV), 1, 0, 1, moe.pack_i8_codes(w).to(DEV), ws.to(DEV),
+                              out_dtype=torch.float32)
+    ref = Q.grouped_linear(xq.numpy(), xs.numpy(), np.arange(rows), offs.tolist(), 1, 1, w.numpy(), ws.numpy())
+    assert np.all(np.abs(f64_of(y) - ref) <= 4 * 2.0 ** -24 * (1 + 1e-6) * np.abs(ref))
+
+
+@pytest.mark.parametrize("d,I", [(64, 64), (4160, 192), (192, 2624), (1088, 1088)])
+def test_ffn_few_rows_long_and_short_sums(d, I):
+    announce(f"ffn few rows {d} {I}")
+    g = _gen(d + I)
+    rows, offs, E, nseg, S, x, ws, ss = _ffn_case(g, dict(sizes=[1, 0, 2, 0, 1], T=3), d, I)
+    h = moe.grouped_ffn_i8(x.to(DEV), offs.to(DEV), E, S, nseg, *_ffn_args(ws, ss), x_rows=rows.to(DEV))
+    torch.cuda.synchronize()
+    _ffn_check(f64_of(h), x, rows, offs, E, nseg, ws, ss)
