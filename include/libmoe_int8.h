@@ -65,8 +65,8 @@ moe_status moe_quantize_rows_i8(const void* x, moe_dtype dtype, int32_t T, int32
  *            an ordinary linear map.
  *   w        [E+n_shared][O][K] int8, packed (above).  w_scale [E+n_shared][O].
  *   y        [n_rows][O] of `out_dtype` (bf16 or fp32), written.
- *   Requires K and O positive multiples of 64, K <= 131072 (the sums of codes in
- *   [-127, 127] stay in int32), nseg in {1, 2}, 1 <= E <= 512, n_shared <= 256; tensors of codes and
+ *   Requires n_rows <= 2^24, K and O positive multiples of 64, K <= 131072 (the
+ *   sums of codes in [-127, 127] stay in int32), nseg in {1, 2}, 1 <= E <= 512, n_shared <= 256; tensors of codes and
  *   values 16-byte aligned, w_scale 16-byte, x_scale 4-byte.
  *   Errors: MOE_ERR_INVALID_ARG for negative sizes, nseg, NULL or misaligned
  *   pointers, n_x < 1 with a row list; MOE_ERR_UNSUPPORTED for the other
@@ -101,7 +101,7 @@ moe_status moe_grouped_linear_i8(const int8_t* xq, const float* x_scale, const i
  *                  (where a row list is given; the query takes x_rows' presence
  *                  from n_x > 0), d and I only.  Calls that share a workspace,
  *                  replayed graphs among them, must not overlap in time.
- *   Requires d and I positive multiples of 64, d <= 131072.
+ *   Requires n_rows <= 2^24, d and I positive multiples of 64, d <= 131072.
  *   Errors: as moe_grouped_ffn_fp8w_packed.
  */
 moe_status moe_grouped_ffn_i8(const void* x_sorted, const int32_t* x_rows, int32_t n_x,

@@ -581,7 +581,7 @@ def test_layer_refuses_what_its_raw_calls_would_read_wrongly():
         layer.bound_calls(z(T, E, dt=f), x)
 
 
-# groups of some 20 and 60 rows, enough of them that every CU has work at 32 and 64 rows a tile
+# groups of some 20 and 60 rows, enough of them that every CU has work at 32 rows a tile
 STREAM = {
     "rows_32": dict(sizes=[14 + (5 * i) % 13 for i in range(64)], T=230, shared=1),
     "rows_64": dict(sizes=[45 + (7 * i) % 31 for i in range(64)], T=150),

@@ -90,7 +90,8 @@ def test_linear_validation(lib):
     for bad in (dict(n_rows=-1), dict(E=0), dict(S=-1), dict(nseg=0), dict(nseg=3), dict(K=0), dict(O=0)):
         assert call(**bad) == INV, bad
     for bad in (dict(E=513), dict(S=257), dict(K=288), dict(O=288), dict(K=131072 + 64), dict(dt=3),
-                dict(n_rows=1 << 24), dict(K=65536, O=65536), dict(rows=FAKE, n_x=1 << 24)):
+                dict(n_rows=1 << 24), dict(K=65536, O=65536), dict(rows=FAKE, n_x=1 << 24),
+                dict(n_rows=(1 << 24) + 1, K=64, O=64)):
         assert call(**bad) == UNS, bad
     for bad in (dict(xq=None), dict(xs=None), dict(offs=None), dict(w=None), dict(ws=None), dict(y=None),
                 dict(xq=FAKE + 8), dict(w=FAKE + 8), dict(ws=FAKE + 4), dict(y=FAKE + 8), dict(offs=FAKE + 2),

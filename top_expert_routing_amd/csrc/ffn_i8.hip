@@ -121,8 +121,8 @@ __device__ __forceinline__ void store4(Out* p, const float (&v)[4]) {
 // columns): each wave owns 16 columns (kGateUp: 16 gate rows and 16 up rows) and
 // reads their weights once; the rows' codes are staged through LDS, 512 of K at a
 // time, double buffered, and shared by the waves.
-// Bound by the weights' bytes: 128 tokens x 8 of 64 experts, 2048 -> 1024, 137 MB in 30 us
-// (4.6 TB/s); an FFN of 1088 tokens x 4 of 128 experts, 2880 x 2880, whose used experts'
+// Bound by the weights' bytes: 128 tokens x 8 of 64 experts, 2048 -> 1024, 137 MB in 28 us
+// (4.8 TB/s); an FFN of 1088 tokens x 4 of 128 experts, 2880 x 2880, whose used experts'
 // weights are 2.7 GB, 551 us (4.95 TB/s, the rate of a copy).  Asking for a step's next
 // weights as soon as it is multiplied, instead of a chunk's together, changes 1 % either
 // way; loads without the branches of a chunk past K are 2 % slower.
@@ -182,7 +182,7 @@ __device__ Item find_item(const ProductArgs& p, int BM, int nch) {
 }
 
 template <int MF, Mode M, class Out>
-__global__ __launch_bounds__(kThreadsS, MF == 4 ? 2 : 4) void stream_i8(ProductArgs p) {
+__global__ __launch_bounds__(kThreadsS, 4) void stream_i8(ProductArgs p) {
   constexpr int BM = 16 * MF;
   constexpr int NF = M == kGateUp ? 2 : 1;
   constexpr int U = kChunk / kStep;
@@ -1035,13 +1035,15 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Rows of stream_i8's tiles, 16 * mf: groups of the average size in one tile.  Where that
-// leaves CUs without an item (at most kIdle... of them), half the rows: two items read the same
-// weights, one from the L2.  us without / with: linear 222 rows x 2048 -> 2048 11.7 / 7.2, 512
-// rows 11.8 / 8.8; FFN of 8 groups of 32 rows, 2048 x 1024, 26.9 / 20.3, 2 of 128 rows, 2048 x
-// 2048, 31.3 / 21.3.  At 200 or 256 items: linear 512 rows 8.8 / 10.0, FFN 16 groups of 64 rows,
-// 1024 x 512, 18.6 / 17.3.
-int pick_mf(int avg) { return avg <= 12 ? 1 : avg <= 28 ? 2 : 4; }
+// Rows of stream_i8's tiles, 16 * mf: 16 for groups that mostly fit (64 groups, 2048 x 1024, with
+// 16 and 32 rows a tile: of 12 rows 79 / 81 us, of 24 rows 88 / 86).  No more than 32: items
+// of the same weights then read them from the L2, but more of them fit on a CU (64 rows a tile: FFN of
+// 481 tokens x 8 of 128 experts, 2240 x 640, 202 us against 161; 700 x 4 of 8, 1472 x 832, 51
+// against 43; a single group of 2048 rows x 2048 -> 2048 21 against 23).  Where CUs are left without
+// an item (at most kIdle... of them), 16 rows: us without / with: linear 300 rows x 2048 -> 1024
+// 8.4 / 6.8; FFN of 8 groups of 32 rows, 2048 x 1024, 22.6 / 20.3.  At 200 or 256 items: linear 512
+// rows 8.8 / 10.0, FFN 16 groups of 64 rows, 1024 x 512, 18.6 / 17.3.
+int pick_mf(int avg) { return avg <= 16 ? 1 : 2; }
 
 // CUs of the current device.
 int device_cus() {
@@ -1065,18 +1067,18 @@ using TileDown = TileWide;
 //                           row, 1024 x 512, 11.8 / 13.4; 64 groups of one row 106 / 75:
 //                           only up to kFewItems items of 128 columns, which also bounds the
 //                           fp32 product to 80 KiB.
-//   stream_i8 or tile_i8    64 rows a group 114 / 113, 96 rows 151 / 117; but linear 2048
-//                           rows (512 items of 64 x 128) 20 / 24, 5800 rows x 2112 -> 832
-//                           (589) 33 / 30, 4096 rows (1024) 38 / 32, 16 groups of 256
-//                           rows, 1024 x 512 (256 items) 34 / 44: tile_i8 needs both full
-//                           tiles and enough of them.  By the product of an FFN: gate/up 384 items 87 / 92, 528 items 93 / 87, 611 items 69 /
-//                           58; down 640 items 83 / 87, 700 items 71 / 76, 768 items 97 / 93,
-//                           917 items 82 / 69.
+//   stream_i8 or tile_i8    64 rows a group 108 / 109, 96 rows 137 / 117; but linear 2048
+//                           rows (512 items of 64 x 128) 23 / 26, 5800 rows x 2112 -> 832
+//                           (589) 35 / 30, 4096 rows (1024) 43 / 31, 16 groups of 256
+//                           rows, 1024 x 512 (256 items) 33 / 39: tile_i8 needs both full
+//                           tiles and enough of them.  By the product of an FFN: gate/up
+//                           384 items 85 / 92, 528 items 93 / 87, 611 items 69 / 58; down 500
+//                           items 57 / 66, 700 items 69 / 76, 917 items 82 / 69.
 //   TileHalf or TileWide    128 rows a group 125 / 130, 192 rows 156 / 147; linear 4096 rows
 //                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
 constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
 constexpr int kIdleLinear = 200, kIdleFfn = 256;
-constexpr int kTileMinAvg = 48;
+constexpr int kTileMinAvg = 64;
 constexpr int tile_min_items(Mode m) { return m == kGateUp ? 512 : m == kDown ? 736 : 576; }
 constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
 constexpr int kWideMinAvg = 192, kWideMinTiles = 256;
@@ -1127,13 +1129,10 @@ void launch_product(const ProductArgs& p, hipStream_t stream) {
   }
   const int nch = (p.cols + kBlock - 1) / kBlock;
   int mf = pick_mf(avg);
-  while (mf > 1 && max_m_tiles(p, 16 * mf) * nch <= (M == kLinear ? kIdleLinear : kIdleFfn)) mf /= 2;
+  if (max_m_tiles(p, 16 * mf) * nch <= (M == kLinear ? kIdleLinear : kIdleFfn)) mf = 1;
   dim3 grid(item_grid(max_m_tiles(p, 16 * mf), nch)), block(kThreadsS);
-  switch (mf) {
-    case 1: hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p); break;
-    default: hipLaunchKernelGGL((stream_i8<4, M, Out>), grid, block, 0, stream, p); break;
-  }
+  if (mf == 1) hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p);
 }
 
 ProductArgs product_args(const GroupedI8& g, int K, int cols) {
