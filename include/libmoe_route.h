@@ -31,7 +31,8 @@ typedef enum { MOE_RANK_MAX = 0, MOE_RANK_TOP2 = 1 } moe_group_rank;
  *
  *   score of expert e   s_e = softmax over the E logits, or sigmoid(logit_e).
  *       (softmax: +inf logits share the mass equally; a row whose logits are
- *       all -inf has scores 0)
+ *       all -inf has scores 0).  Scores are doubles: what rounds to 0 there (below
+ *       2^-1075, a sigmoid of less than about -745.1) is 0.
  *   choice value        c_e = s_e + bias_e in double, NaN as -inf; without a
  *       bias the experts are ordered by their logits, whose order is the scores'.
  *   groups              the E experts form n_groups groups of E / n_groups
@@ -44,7 +45,8 @@ typedef enum { MOE_RANK_MAX = 0, MOE_RANK_TOP2 = 1 } moe_group_rank;
  *       expert id.  An expert of -inf choice value comes after all others.
  *   topk_w   [T][k] fp32, written: scale * s_id (renormalize = 0), or
  *       scale * s_id / (sum of the k chosen scores) (renormalize = 1; all 0
- *       where that sum is 0).  Within 1e-6 relative of the exact value.
+ *       where that sum is 0).  Within 1e-6 relative of the exact value, or 2^-149
+ *       where that is more (results next to fp32's subnormals).
  *
  *   Requires T >= 0, 1 <= n_groups <= 64, E a multiple of n_groups,
  *   1 <= top_groups <= n_groups, 1 <= k <= top_groups * (E / n_groups),

@@ -7,7 +7,9 @@ import numpy as np
 
 def route(logits, k, score="softmax", bias=None, n_groups=1, top_groups=1, group_rank="max", renormalize=True,
           scale=1.0):
-    """ids [T][k] int32 and weights [T][k] float64 of logits [T][E]."""
+    """ids [T][k] int32 and weights [T][k] float64 of logits [T][E].  Scores that decide
+    are doubles; weights are taken from scores in long double, whose exponents reach
+    further, unless the chosen doubles sum to 0."""
     l = np.array(logits, dtype=np.float64)
     l[np.isnan(l)] = -np.inf
     T, E = l.shape
@@ -17,13 +19,17 @@ def route(logits, k, score="softmax", bias=None, n_groups=1, top_groups=1, group
     for t in range(T):
         row = l[t]
         with np.errstate(over="ignore", invalid="ignore"):
+            wide = row.astype(np.longdouble)
             if score == "sigmoid":
-                s = 1.0 / (1.0 + np.exp(-row))
+                s = np.where(row < -700, np.exp(row), 1.0 / (1.0 + np.exp(-row)))
+                wide = 1 / (1 + np.exp(-wide))
             elif np.all(row == -np.inf):
-                s = np.zeros(E)
+                s = wide = np.zeros(E)
             else:
                 z = np.where(row == row.max(), 1.0, np.exp(row - row.max()))
                 s = z / z.sum()
+                wide = np.where(row == row.max(), np.longdouble(1), np.exp(wide - wide.max()))
+                wide = wide / wide.sum()
             c = row.copy() if bias is None else s + np.asarray(bias, np.float64)
         c[np.isnan(c)] = -np.inf
         chosen = []
@@ -37,10 +43,9 @@ def route(logits, k, score="softmax", bias=None, n_groups=1, top_groups=1, group
         allowed = [e for e in range(E) if e // size in kept]
         order = sorted(allowed, key=lambda e: (-c[e], e))[:k]
         ids[t] = order
-        w[t] = s[order]
+        w[t] = wide[order]
         if renormalize:
-            total = w[t].sum()
-            w[t] = w[t] / total if total > 0 else 0.0
+            w[t] = wide[order] / wide[order].sum() if s[order].sum() > 0 else 0.0
     return ids, w * float(np.float32(scale))
 
 

@@ -1,0 +1,69 @@
+"""Routing with scores and the int8 calls at the ends of their documented ranges, against the float64 definitions."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8_oracle as Q
+from helpers import announce, f64_of, np_of, require_gpu
+
+import top_expert_routing_amd as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------ route
+def _tiny_scores(g, k, score):
+    """Rows whose k best logits give scores near and below the smallest normal double.  Softmax: one expert that the
+    bias keeps out has all the mass."""
+    tops = [-700.0, -706.0, -708.0, -709.0, -709.3, -709.7, -709.9, -720.0, -740.0, -744.0, -745.0, -745.25, -760.0, -250.0, -490.0]
+    E = 32
+    l = torch.full((2 * len(tops), E), -790.0)
+    for i, top in enumerate(tops):
+        l[2 * i, 1:1 + k] = top                                            # equal scores
+        l[2 * i + 1, 1:1 + k] = top - 3 * torch.rand(k, generator=g)       # unequal ones
+    if score == "softmax":
+        l[:, 0] = 0.0
+    bias = torch.zeros(E)
+    bias[0] = -10.0
+    bias[1:1 + k] = 1.0
+    return l, bias
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 8])
+@pytest.mark.parametrize("scale", [1.0, 2.5, 16.0, -3.0e38])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_tiny_scores(score, k, scale, renorm):
+    """The weights of chosen experts whose scores sum to next to nothing are still their shares of the scale."""
+    announce(f"route tiny scores {score} {k} {scale} {renorm}")
+    l, bias = _tiny_scores(_gen(21), k, score)
+    for dtype in (torch.float32, torch.bfloat16):
+        lt = l.to(dtype)
+        ids, w = moe.route(lt.to(DEV), k, score, bias.to(DEV), renormalize=renorm, scale=scale)
+        ref_ids, ref_w = Q.route(f64_of(lt), k, score, f64_of(bias), renormalize=renorm, scale=scale)
+        np.testing.assert_array_equal(np_of(ids), ref_ids)
+        got = f64_of(w)
+        assert np.isfinite(got).all()
+        # the call's promise: 1e-6 of the value, or 2^-149
+        assert np.all(np.abs(got - ref_w) <= np.maximum(1e-6 * np.abs(ref_w), 2.0 ** -149))
+        if renorm:
+            assert (np.abs(ref_w).sum(1) > 0).sum() > len(lt) // 2
+
+
+def test_route_tiny_scores_order_groups():
+    """Sums of sigmoids below e^-709.8 still tell the groups apart."""
+    l = torch.full((2, 16), -800.0)
+    l[0, 0:2], l[0, 12:14] = -740.0, -712.0
+    l[1, 4:6], l[1, 8:10] = -712.0, -710.0
+    ids, w = moe.route(l.to(DEV), 2, "sigmoid", n_groups=4, top_groups=1, group_rank="top2")
+    assert ids.tolist() == [[12, 13], [8, 9]] and w.tolist() == [[0.5, 0.5]] * 2

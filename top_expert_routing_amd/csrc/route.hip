@@ -143,6 +143,15 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock, P <= 4 ? 8 : P <= 6 ? 6 : 5
   if (a.sigmoid) {
 #pragma unroll
     for (int i = 0; i < P; ++i) s[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
+    // far below zero 1 + exp(-l) leaves the doubles and exp(l) is the score to its last bit
+    bool low = false;
+#pragma unroll
+    for (int i = 0; i < P; ++i) low |= l[i] < -700.0f && l[i] > -__builtin_inff();
+    if (__any(low)) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (l[i] < -700.0f) s[i] = exp(static_cast<double>(l[i]));
+    }
   } else {
     float m = l[0];
 #pragma unroll
@@ -280,10 +289,33 @@ __global__ __launch_bounds__(kWave * kWavesPerBlock, P <= 4 ? 8 : P <= 6 ? 6 : 5
 #pragma unroll
     for (int i = 0; i < P; ++i) hi[i] = __builtin_amdgcn_inverse_ballot_w64(m[i]) ? static_cast<uint32_t>(r) : hi[i];
   }
-  double sum = 0.0;
+  auto sum_chosen = [&]() {
+    double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < P; ++i) sum += hi[i] - 1u < static_cast<uint32_t>(a.k) ? s[i] : 0.0;
-  const double denom = a.renormalize ? wave_sum_d(sum) : 1.0;
+    for (int i = 0; i < P; ++i) sum += hi[i] - 1u < static_cast<uint32_t>(a.k) ? s[i] : 0.0;
+    return wave_sum_d(sum);
+  };
+  double denom = a.renormalize ? sum_chosen() : 1.0;
+  if (denom > 0.0 && denom < 0x1p-700) {        // wave-uniform
+    // Scores this small lose bits (below 2^-1022) and scale / denom can leave the doubles, but their
+    // quotients are those of the exponentials of the logits, here taken relative to the largest chosen one
+    // (all are finite: a sum of scores with an infinite logit is 0 or not small).
+    float z[P], m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      z[i] = -__builtin_inff();
+      if (hi[i] - 1u < static_cast<uint32_t>(a.k)) {
+        if constexpr (BF16) z[i] = bf16_to_f32(row[i]);
+        else z[i] = row[i];
+        if (z[i] != z[i]) z[i] = -__builtin_inff();
+      }
+      m = fmaxf(m, z[i]);
+    }
+    m = wave_max_f(m);
+#pragma unroll
+    for (int i = 0; i < P; ++i) s[i] = exp(static_cast<double>(z[i]) - static_cast<double>(m));
+    denom = sum_chosen();
+  }
   const double factor = denom > 0.0 ? static_cast<double>(a.scale) / denom : 0.0;
   // each lane writes its chosen experts at their places
   const size_t at = static_cast<size_t>(t) * a.k;
