@@ -67,3 +67,17 @@ def test_route_tiny_scores_order_groups():
     l[1, 4:6], l[1, 8:10] = -712.0, -710.0
     ids, w = moe.route(l.to(DEV), 2, "sigmoid", n_groups=4, top_groups=1, group_rank="top2")
     assert ids.tolist() == [[12, 13], [8, 9]] and w.tolist() == [[0.5, 0.5]] * 2
+
+
+# ------------------------------------------------------------------ quantize
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [2 ** 31 - 8, 2 ** 31 - 2048, 2 ** 30 + 8])
+def test_quantize_longest_rows(d, dtype):
+    """One row of nearly 2^31 values: the loop's last step passes int32 for some of the lanes."""
+    announce(f"quantize longest row {d} {dtype}")
+    x = torch.zeros((1, d), dtype=dtype, device=DEV)
+    where = torch.cat([torch.arange(0, d, 16777259), torch.arange(d - 4096, d)]).to(DEV)
+    x[0, where] = (torch.arange(len(where), device=DEV) % 255 - 127).to(dtype)        # scale 1: codes are the values
+    q, s = moe.quantize_rows_i8(x)
+    assert s.tolist() == [1.0]
+    assert torch.equal(q, x.to(torch.int8))

@@ -67,7 +67,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows(const void* __restrict
     for (int h = 0; h < HELD; ++h)
       if ((h * LANES + l) * 8 < d) m = max(m, piece_max(held[h]));
   } else {
-    for (int i = l * 8; i < d; i += LANES * 8) m = max(m, piece_max(load8<BF16>(x, row + i)));
+    // unsigned: the last step of a row next to 2^31 values passes int32
+    for (uint32_t i = l * 8; i < static_cast<uint32_t>(d); i += LANES * 8) m = max(m, piece_max(load8<BF16>(x, row + i)));
   }
 #pragma unroll
   for (int o = kWave / 2; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, kWave)));
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows(const void* __restrict
       if (i < d) *reinterpret_cast<uint2*>(q + row + i) = quant_codes8(held[h].v, qs);
     }
   } else {
-    for (int i = l * 8; i < d; i += LANES * 8)
+    for (uint32_t i = l * 8; i < static_cast<uint32_t>(d); i += LANES * 8)
       *reinterpret_cast<uint2*>(q + row + i) = quant_codes8(load8<BF16>(x, row + i).v, qs);
   }
   if (l == 0) s[t] = qs.scale;
