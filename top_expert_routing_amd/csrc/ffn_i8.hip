@@ -21,7 +21,7 @@
 #include <type_traits>
 
 #include "common.h"
-#include "item_plan.h"
+#include "i8_plan.h"
 #include "launch.h"
 #include "quantize.h"
 
@@ -34,10 +34,9 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // Lambdas over the kernel's state: a call that is not inlined would put that state in memory.
 #define MOE_INLINE __attribute__((always_inline))
 
-enum Mode { kLinear, kGateUp, kDown };
+using namespace i8;
 
-constexpr int kBlock = 128;          // columns of the SwiGLU product that share a scale
-constexpr int kStep = 64;            // K of one matrix instruction
+static_assert(kLanes == kWave, "one wavefront");
 constexpr int kMaxGroups = 2 * 512 + 256;
 
 struct ProductArgs {
@@ -571,35 +570,6 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs
 // 2 or 8 column chunks, tiles of equal height within a group, skipping the operand reads of
 // empty blocks, one barrier for two steps (it has to wait for every load and read: 81 us and
 // 278); each within 2 % or slower.
-template <int MI_, int NJ_, int WM_, int WN_, int BPC_>
-struct TileCfg {
-  static constexpr int BPC = BPC_;                             // blocks per CU
-  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = kWave * NW;
-  static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
-  static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;
-  static_assert(ADMA >= 1 && ADMA <= 4 && BDMA >= 1, "DMA instructions per wave");
-};
-constexpr int kLdsPerCu = 160 * 1024;
-template <class C, Mode M>
-struct TileLds {
-  static constexpr int SUB = M == kDown ? 2 : 1;               // K steps per stage
-  static constexpr int A = C::BM * kStep, B = C::BN * kStep;   // bytes per K step
-  static constexpr int WROWS = 16 * C::ADMA * 4;               // one 4-byte value per row: of a wave's loads, of all
-  static constexpr int ROWS = C::NW * WROWS;
-  static constexpr int STAGE = SUB * (A + B) + (M == kDown ? ROWS : 0);
-  // as many as fit beside 12 KiB (two blocks per CU: 8) of lists, scales and the plan
-  static constexpr int STAGES = (kLdsPerCu / C::BPC - (C::BPC == 2 ? 8 : 12) * 1024) / STAGE;
-  static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
-  static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
-  static constexpr int RING = STAGES * STAGE;
-  static constexpr int LIST = RING;                            // row list of two tiles
-  static constexpr int SA = LIST + 2 * ROWS;                   // row scales of two tiles
-  static constexpr int SB = SA + 2 * ROWS;                     // channel scales of two tiles
-  static constexpr int MAX = SB + 2 * 1024;                    // kGateUp: largest magnitudes
-  static constexpr int PLAN = MAX + C::WN * C::BM * 4;         // sums over waves, tiles before each group, group offsets
-  static int bytes(int G) { return PLAN + 4 * C::NW + 8 * (G + 1); }
-};
-
 __device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
 
 // LDS-DMA loads: each lane's 16 or 4 bytes go to LDS address lds + 16 (or 4) * lane.
@@ -1035,16 +1005,6 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Rows of stream_i8's tiles, 16 * mf: 16 for groups that mostly fit (64 groups, 2048 x 1024, with
-// 16 and 32 rows a tile: of 12 rows 79 / 81 us, of 24 rows 88 / 86).  No more than 32: items
-// of the same weights then read them from the L2, but more of them fit on a CU (64 rows a tile: FFN of
-// 481 tokens x 8 of 128 experts, 2240 x 640, 202 us against 161; 700 x 4 of 8, 1472 x 832, 51
-// against 43; a single group of 2048 rows x 2048 -> 2048 21 against 23).  Where CUs are left without
-// an item (at most kIdle... of them), 16 rows: us without / with: linear 300 rows x 2048 -> 1024
-// 8.4 / 6.8; FFN of 8 groups of 32 rows, 2048 x 1024, 22.6 / 20.3.  At 200 or 256 items: linear 512
-// rows 8.8 / 10.0, FFN 16 groups of 64 rows, 1024 x 512, 18.6 / 17.3.
-int pick_mf(int avg) { return avg <= 16 ? 1 : 2; }
-
 // CUs of the current device.
 int device_cus() {
   int dev = 0, cus = 0;
@@ -1054,55 +1014,12 @@ int device_cus() {
   return cus;
 }
 
-using TileWide = TileCfg<4, 8, 4, 2, 1>;   // 256 rows, one block of eight waves per CU
-using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves per CU
-using TileDown = TileWide;
-
-// Which kernel: the host sees the average group, not the groups.  Times of the whole call,
-// us; d, I or K, O = 2048, 1024 (FFN, 64 groups) and 2048, 2048 (linear, one group).
-//   few_i8 or stream_i8     linear 16 rows 4.8 / 6.7, 128 rows 6.1 / 6.8, 256 rows 9.9 /
-//                           7.2: few_i8 up to kFewBlocksMost items of 16 x 16 (1024 x 512,
-//                           512 rows 5.5 / 5.6, 1024 rows 9.2 / 7.1).  FFN with 8 groups of
-//                           one row 16.2 / 18.4, of 8 rows 23.8 / 19.2; 16 groups of one
-//                           row, 1024 x 512, 11.8 / 13.4; 64 groups of one row 106 / 75:
-//                           only up to kFewItems items of 128 columns, which also bounds the
-//                           fp32 product to 80 KiB.
-//   stream_i8 or tile_i8    64 rows a group 108 / 109, 96 rows 137 / 117; but linear 2048
-//                           rows (512 items of 64 x 128) 23 / 26, 5800 rows x 2112 -> 832
-//                           (589) 35 / 30, 4096 rows (1024) 43 / 31, 16 groups of 256
-//                           rows, 1024 x 512 (256 items) 33 / 39: tile_i8 needs both full
-//                           tiles and enough of them.  By the product of an FFN: gate/up
-//                           384 items 85 / 92, 528 items 93 / 87, 611 items 69 / 58; down 500
-//                           items 57 / 66, 700 items 69 / 76, 917 items 82 / 69.
-//   TileHalf or TileWide    128 rows a group 125 / 130, 192 rows 156 / 147; linear 4096 rows
-//                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
-constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
-constexpr int kIdleLinear = 200, kIdleFfn = 256;
-constexpr int kTileMinAvg = 64;
-constexpr int tile_min_items(Mode m) { return m == kGateUp ? 512 : m == kDown ? 736 : 576; }
-constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
-constexpr int kWideMinAvg = 192, kWideMinTiles = 256;
-
-bool few(int n_rows, int cols) { return static_cast<long long>(n_rows) * ((cols + kBlock - 1) / kBlock) <= kFewItems; }
-
-// m-tiles of BM rows of a call, at most: ceil(n / BM) <= 1 + (n - 1) / BM for each group with rows.
-int max_m_tiles(const ProductArgs& p, int BM) {
-  const int groups = p.G < p.n_rows ? p.G : p.n_rows;
-  return groups + (p.n_rows - groups) / BM;
-}
-
 template <Mode M, class Out>
-void launch_few(const ProductArgs& p, hipStream_t stream) {
-  const int tiles = max_m_tiles(p, 16), blocks16 = tiles * (p.cols / 16);
-  auto grid = [&](int nc) { return dim3(item_grid(tiles, p.cols / (16 * nc))); };
-  // wider items where 16 columns give more blocks than run at once (a block is mostly waits:
-  // 1024 of them took 10.7 us for one token's down product, 256 of 64 columns 5 us)
-  if (blocks16 <= kFewBlocks)
-    hipLaunchKernelGGL((few_i8<1, M, Out>), grid(1), dim3(kThreadsS), 0, stream, p);
-  else if (M == kGateUp || blocks16 <= 2 * kFewBlocks)
-    hipLaunchKernelGGL((few_i8<2, M, Out>), grid(2), dim3(kThreadsS), 0, stream, p);
-  else
-    hipLaunchKernelGGL((few_i8<M == kGateUp ? 2 : 4, M, Out>), grid(4), dim3(kThreadsS), 0, stream, p);
+void launch_few(const ProductArgs& p, const Plan& plan, hipStream_t stream) {
+  const dim3 grid(plan.blocks), block(kThreadsS);
+  if (plan.width == 1) hipLaunchKernelGGL((few_i8<1, M, Out>), grid, block, 0, stream, p);
+  else if (plan.width == 2) hipLaunchKernelGGL((few_i8<2, M, Out>), grid, block, 0, stream, p);
+  else if constexpr (M != kGateUp) hipLaunchKernelGGL((few_i8<4, M, Out>), grid, block, 0, stream, p);
 }
 
 template <class Tile, Mode M, class Out>
@@ -1113,27 +1030,19 @@ void launch_tile(const ProductArgs& p, hipStream_t stream) {
 }
 
 template <Mode M, class Out>
-void launch_product(const ProductArgs& p, hipStream_t stream) {
-  const int avg = p.n_rows / p.G;
-  const long long area = static_cast<long long>(p.n_rows) * p.cols;
-  if (avg > kTileMinAvg && p.K >= kTileMinK && area >= tile_min_items(M) * 64ll * 128) {
-    const long long wide = area / (256 * (M == kGateUp ? 128 : 256));
-    // (the lists of two blocks per CU have room for some 380 groups)
-    if (M == kDown || (avg >= kWideMinAvg && wide >= kWideMinTiles) ||
-        TileLds<TileHalf, M == kDown ? kLinear : M>::bytes(p.G) > kLdsPerCu / 2) {
-      launch_tile<std::conditional_t<M == kDown, TileDown, TileWide>, M, Out>(p, stream);
-    } else if constexpr (M != kDown) {
-      launch_tile<TileHalf, M, Out>(p, stream);
-    }
-    return;
+void launch_many(const ProductArgs& p, const Plan& plan, hipStream_t stream) {
+  if (plan.kernel == Kernel::kStream) {
+    const dim3 grid(plan.blocks), block(kThreadsS);
+    if (plan.width == 1) hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p);
+  } else if (plan.kernel == Kernel::kTileWide) {
+    launch_tile<TileWide, M, Out>(p, stream);
+  } else if constexpr (M != kDown) {
+    launch_tile<TileHalf, M, Out>(p, stream);
   }
-  const int nch = (p.cols + kBlock - 1) / kBlock;
-  int mf = pick_mf(avg);
-  if (max_m_tiles(p, 16 * mf) * nch <= (M == kLinear ? kIdleLinear : kIdleFfn)) mf = 1;
-  dim3 grid(item_grid(max_m_tiles(p, 16 * mf), nch)), block(kThreadsS);
-  if (mf == 1) hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p);
 }
+
+Sizes sizes_of(const ProductArgs& p) { return Sizes{p.n_rows, p.E, p.G - p.nseg * p.E, p.nseg, p.K, p.cols}; }
 
 ProductArgs product_args(const GroupedI8& g, int K, int cols) {
   ProductArgs p{};
@@ -1173,13 +1082,14 @@ hipError_t launch_grouped_linear_i8(const GroupedI8& g, const int8_t* xq, const 
   p.w0 = w;
   p.s0 = ws;
   p.out = y;
-  if (static_cast<long long>(max_m_tiles(p, 16)) * (O / 16) <= kFewBlocksMost) {
-    if (bf16) launch_few<kLinear, uint16_t>(p, stream);
-    else launch_few<kLinear, float>(p, stream);
-    return hipGetLastError();
+  const Plan plan = plan_linear(sizes_of(p));
+  if (plan.kernel == Kernel::kFew) {
+    if (bf16) launch_few<kLinear, uint16_t>(p, plan, stream);
+    else launch_few<kLinear, float>(p, plan, stream);
+  } else {
+    if (bf16) launch_many<kLinear, uint16_t>(p, plan, stream);
+    else launch_many<kLinear, float>(p, plan, stream);
   }
-  if (bf16) launch_product<kLinear, uint16_t>(p, stream);
-  else launch_product<kLinear, float>(p, stream);
   return hipGetLastError();
 }
 
@@ -1198,13 +1108,13 @@ hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream
     p.s0 = a.s_gate;
     p.s1 = a.s_up;
     p.out = ws + L.aq;
-    launch_few<kGateUp, float>(p, stream);
+    launch_few<kGateUp, float>(p, plan_ffn(kGateUp, sizes_of(p)), stream);
     ProductArgs h = product_args(a.g, a.I, a.d);
     h.af = reinterpret_cast<const float*>(ws + L.aq);
     h.w0 = a.w_down;
     h.s0 = a.s_down;
     h.out = a.h_sorted;
-    launch_few<kDown, uint16_t>(h, stream);
+    launch_few<kDown, uint16_t>(h, plan_ffn(kDown, sizes_of(h)), stream);
     return hipGetLastError();
   }
   int8_t* xq = reinterpret_cast<int8_t*>(ws);
@@ -1220,7 +1130,7 @@ hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream
   p.s1 = a.s_up;
   p.out = ws + L.aq;
   p.out_scale = reinterpret_cast<float*>(ws + L.as);
-  launch_product<kGateUp, int8_t>(p, stream);
+  launch_many<kGateUp, int8_t>(p, plan_ffn(kGateUp, sizes_of(p)), stream);
   ProductArgs h = product_args(a.g, a.I, a.d);
   h.x_rows = nullptr;                       // the SwiGLU product is in sorted order
   h.n_x = a.g.n_rows;
@@ -1229,7 +1139,7 @@ hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream
   h.w0 = a.w_down;
   h.s0 = a.s_down;
   h.out = a.h_sorted;
-  launch_product<kDown, uint16_t>(h, stream);
+  launch_many<kDown, uint16_t>(h, plan_ffn(kDown, sizes_of(h)), stream);
   return hipGetLastError();
 }
 
