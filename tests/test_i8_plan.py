@@ -1,6 +1,7 @@
 """Which kernel an int8 product runs on, and how it is launched (CPU only)."""
 import itertools
 
+import numpy as np
 import pytest
 
 import i8_plan
@@ -25,3 +26,45 @@ def test_both_products_of_few_rows_agree(E, S, nseg):
         up, down = i8_plan.ffn(n, E, S, nseg, d, I)
         assert (up[0] == "few") == (down[0] == "few"), (n, d, I)
         assert up[1] in (0, 1, 2) and down[1] in (0, 1, 2, 4)
+
+
+# (E, shared, K or d, O or I) of batches with a priority segment, small to large
+PRIORITY = [(128, 0, 2880, 2880), (64, 0, 2048, 1024), (16, 1, 1024, 512), (8, 2, 256, 1344), (300, 4, 512, 512)]
+
+
+@pytest.mark.parametrize("E,S,d,I", PRIORITY)
+def test_a_priority_segment_does_not_change_the_kernels(E, S, d, I):
+    """Tiles take an expert's rows of both segments as one sequence, so the rows of an expert decide, however many
+    groups they lie in (but for the 128-row tiles, whose lists hold fewer groups)."""
+    queries = [(n, E, S) for n in range(1, 300 * E, max(1, E // 3))]
+    plan = lambda nseg: i8_plan.ask([q for n, E, S in queries for q in
+                                     (("linear", n, E, S, nseg, d, I), ("gate_up", n, E, S, nseg, d, I), ("down", n, E, S, nseg, I, d))])
+    for one, two, q in zip(plan(1), plan(2), [n for n, _, _ in queries for _ in range(3)]):
+        if two[0] == "tile_wide" and one[0] == "tile_half" and 2 * E + S > 380:
+            continue
+        assert one == two, (q, one, two)
+
+
+@pytest.mark.parametrize("E,nseg,shared", [(4, 1, 0), (4, 2, 1), (70, 2, 0), (33, 1, 3)])
+def test_the_grid_holds_every_tile(E, nseg, shared):
+    """No XCD has more (tile, column chunk) items than the launch gives it blocks."""
+    rng = np.random.default_rng(E + nseg)
+    for O in (64, 448, 1152, 2048):
+        for most in (1, 3, 17, 40):
+            sizes = rng.integers(0, most + 1, (nseg, E))
+            n = int(sizes.sum()) + 5 * shared
+            if n == 0:
+                continue
+            kernel, width, blocks = i8_plan.linear(n, E, shared, nseg, 192, O)
+            bm, columns = (16, 16 * width) if kernel == "few" else (16 * width, 128)
+            chunks = -(-O // columns)
+            up = lambda rows: -(-rows // bm)
+            tiles = [up(sizes[0, e]) for e in range(E)]                      # of each group, in group order
+            if nseg == 2:
+                tiles += [up(sizes[:, e].sum()) - up(sizes[0, e]) for e in range(E)]
+            tiles += [up(5)] * shared
+            items = np.zeros(8, int)
+            for g, t in enumerate(tiles):
+                for j in range(chunks):
+                    items[(g * chunks + j) % 8] += t
+            assert blocks % 8 == 0 and items.max() <= blocks // 8, (O, most, kernel)

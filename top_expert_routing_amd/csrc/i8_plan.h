@@ -65,6 +65,10 @@ using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves
 //                           items 57 / 66, 700 items 69 / 76, 917 items 82 / 69.
 //   TileHalf or TileWide    128 rows a group 125 / 130, 192 rows 156 / 147; linear 4096 rows
 //                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
+// Averages are rows per sequence that tiles are cut from (Sizes::sequences), not per group: with
+// 64 priority tokens, 128 experts x 4, 2880 x 2880, by group / by sequence: 1024 tokens 985 / 746,
+// 3072 tokens 1333 / 887, 4096 tokens 1535 / 967, 4160 tokens 969 / 966, 6144 tokens 1214 / 1084;
+// 64 experts x 8, 2048 x 1024: 256 tokens 136 / 109, 1024 tokens 211 / 152, 2048 tokens 212 / 181.
 constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
 constexpr int kIdleLinear = 200, kIdleFfn = 256;
 constexpr int kTileMinAvg = 64;
@@ -82,20 +86,21 @@ constexpr int kWideMinAvg = 192, kWideMinTiles = 256;
 // rows 8.8 / 10.0, FFN 16 groups of 64 rows, 1024 x 512, 18.6 / 17.3.
 inline int pick_mf(int avg) { return avg <= 16 ? 1 : 2; }
 
-
 // A product of n_rows sorted rows in nseg * E + n_shared groups with matrices [cols][K].
 struct Sizes {
   int n_rows, E, n_shared, nseg, K, cols;
   int groups() const { return nseg * E + n_shared; }
+  // Row sequences that tiles are cut from: an expert's rows of both segments form one (group_rows).
+  int sequences() const { return E + n_shared; }
 };
 
 // The FFN's products of few rows (both of them: the SwiGLU product is kept in fp32 then).
 inline bool few(int n_rows, int I) { return static_cast<long long>(n_rows) * ((I + kBlock - 1) / kBlock) <= kFewItems; }
 
-// m-tiles of BM rows of a call, at most: ceil(n / BM) <= 1 + (n - 1) / BM for each group with rows.
+// m-tiles of BM rows of a call, at most: ceil(n / BM) <= 1 + (n - 1) / BM for each sequence with rows.
 inline int max_m_tiles(const Sizes& s, int BM) {
-  const int groups = s.groups() < s.n_rows ? s.groups() : s.n_rows;
-  return groups + (s.n_rows - groups) / BM;
+  const int sequences = s.sequences() < s.n_rows ? s.sequences() : s.n_rows;
+  return sequences + (s.n_rows - sequences) / BM;
 }
 
 enum class Kernel { kFew, kStream, kTileHalf, kTileWide };
@@ -114,7 +119,7 @@ inline Plan plan_few(Mode m, const Sizes& s) {
 }
 
 inline Plan plan_many(Mode m, const Sizes& s) {
-  const int avg = s.n_rows / s.groups();
+  const int avg = s.n_rows / s.sequences();
   const long long area = static_cast<long long>(s.n_rows) * s.cols;
   if (avg > kTileMinAvg && s.K >= kTileMinK && area >= tile_min_items(m) * 64ll * 128) {
     const long long wide = area / (256 * (m == kGateUp ? 128 : 256));
