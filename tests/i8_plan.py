@@ -24,13 +24,18 @@ def _program():
     return exe, folder
 
 
-def ask(queries):
-    """(kernel, width, blocks) of each (product, n_rows, E, n_shared, nseg, K, cols)."""
+def launches(queries):
+    """(kernel, width, blocks, grid x, grid y) of each (product, n_rows, E, n_shared, nseg, K, cols)."""
     text = "".join(" ".join(map(str, q)) + "\n" for q in queries)
     out = subprocess.run([_program()[0]], input=text, capture_output=True, text=True, check=True, timeout=60).stdout
-    plans = [(k, int(w), int(b)) for k, w, b in (line.split() for line in out.splitlines())]
+    plans = [(line.split()[0], *map(int, line.split()[1:])) for line in out.splitlines()]
     assert len(plans) == len(queries)
     return plans
+
+
+def ask(queries):
+    """(kernel, width, blocks) of each of them."""
+    return [p[:3] for p in launches(queries)]
 
 
 def linear(n_rows, E, n_shared, nseg, K, O):

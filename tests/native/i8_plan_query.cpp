@@ -1,6 +1,6 @@
 // Prints the kernel that the library picks for int8 products: one line
 // "product n_rows E n_shared nseg K cols" in (product: linear, gate_up, down), one line
-// "kernel width blocks" out.
+// "kernel width blocks x y" out (x, y: the launch's grid).
 #include <cstdio>
 #include <cstring>
 
@@ -15,7 +15,8 @@ int main() {
     const Plan p = !std::strcmp(product, "linear") ? plan_linear(s)
                                                    : plan_ffn(std::strcmp(product, "down") ? kGateUp : kDown, s);
     const char* names[] = {"few", "stream", "tile_half", "tile_wide"};
-    std::printf("%s %d %d\n", names[static_cast<int>(p.kernel)], p.width, p.blocks);
+    const Launch l = launch_of(p);
+    std::printf("%s %d %d %d %d\n", names[static_cast<int>(p.kernel)], p.width, p.blocks, l.x, l.y);
   }
   return 0;
 }

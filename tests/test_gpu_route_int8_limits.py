@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from oracle import int8_oracle as Q
+import i8_plan
 from helpers import announce, f64_of, np_of, require_gpu
 
 import top_expert_routing_amd as moe
@@ -81,3 +82,29 @@ def test_quantize_longest_rows(d, dtype):
     q, s = moe.quantize_rows_i8(x)
     assert s.tolist() == [1.0]
     assert torch.equal(q, x.to(torch.int8))
+
+
+# ------------------------------------------------------------------ the widest matrices
+def test_linear_more_blocks_than_one_row_of_a_launch():
+    """33 experts of one row each and 32.5 million output channels: 2^23 + 256 blocks of 512 threads."""
+    E, K, O = 33, 64, 32537728
+    announce(f"linear {E} x {K} -> {O}")
+    kernel, _, blocks, x, y = i8_plan.launches([("linear", E, E, 0, 1, K, O)])[0]
+    assert kernel == "stream" and blocks * 512 >= 2 ** 32 and y > 1
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("needs 69 GB of weights")
+    g = _gen(22)
+    xq = torch.randint(-127, 128, (E, K), generator=g, dtype=torch.int8).to(DEV)
+    xs = (torch.rand(E, generator=g) + 0.5).to(DEV)
+    w = torch.ones((E, O, K), dtype=torch.int8, device=DEV)          # the same in any order of codes
+    ws = torch.rand((E, O), device=DEV) + 0.5
+    y = torch.zeros((E, O), dtype=torch.bfloat16, device=DEV)
+    offs = torch.arange(E + 1, dtype=torch.int32, device=DEV)
+    moe.grouped_linear_i8(xq, xs, offs, E, 0, 1, w, ws, y)
+    sums = xq.double().sum(1)
+    tol = (3 * 2.0 ** -24 + torch.finfo(torch.bfloat16).eps / 2) * (1 + 1e-6)
+    for e in range(E):
+        ref = sums[e] * xs[e].double() * ws[e].double()
+        assert bool(((y[e].double() - ref).abs() <= tol * ref.abs()).all()), e
+    del w, ws, y
+    torch.cuda.empty_cache()

@@ -68,3 +68,22 @@ def test_the_grid_holds_every_tile(E, nseg, shared):
                 for j in range(chunks):
                     items[(g * chunks + j) % 8] += t
             assert blocks % 8 == 0 and items.max() <= blocks // 8, (O, most, kernel)
+
+
+def test_launches_stay_below_two_to_the_32_threads():
+    """Every launch of 512-thread blocks that the sizes allow (codes, values and matrices below 2^31) has fewer than
+    2^32 threads along x, all the plan's blocks, and XCDs dealt as in one row of blocks."""
+    queries = []
+    for E, S, nseg in ((1, 0, 1), (64, 0, 1), (512, 256, 1), (512, 256, 2)):
+        for n in (1, 33, 64, 160, 768, 1280, 2000, 20480, 1 << 17, 1 << 24):
+            for K in (64, 192, 1024, 131072):
+                most = min((2 ** 31 - 1) // n, (2 ** 31 - 1) // K)
+                for O in {64, 448, most // 64 * 64, most // 128 * 64}:
+                    if O and n * K < 2 ** 31:
+                        queries += [("linear", n, E, S, nseg, K, O), ("gate_up", n, E, S, nseg, K, O), ("down", n, E, S, nseg, O, K)]
+    over = 0
+    for q, (kernel, width, blocks, x, y) in zip(queries, i8_plan.launches(queries)):
+        assert 0 <= blocks <= 2 ** 25 and x * 512 < 2 ** 32 and y <= 65535, q
+        assert x * y >= blocks and (y == 1 or x % 8 == 0), q
+        over += blocks * 512 >= 2 ** 32
+    assert over > 4                       # some need more than one row

@@ -165,7 +165,7 @@ moe_status grouped_i8_sizes(int32_t n_rows, int32_t E, int32_t n_shared, int32_t
   if (n_rows < 0 || E < 1 || n_shared < 0 || (nseg != 1 && nseg != 2) || K < 1 || O < 1) return MOE_ERR_INVALID_ARG;
   if (E > MOE_MAX_EXPERTS || n_shared > MOE_MAX_SHARED) return MOE_ERR_UNSUPPORTED;
   if (K % 64 != 0 || O % 64 != 0 || K > 131072) return MOE_ERR_UNSUPPORTED;
-  if (n_rows > 1 << 24) return MOE_ERR_UNSUPPORTED;   // a launch's threads stay below 2^32
+  if (n_rows > 1 << 24) return MOE_ERR_UNSUPPORTED;   // keeps a launch within 2^25 blocks
   if (!fits_int(static_cast<long long>(n_rows) * K) || !fits_int(static_cast<long long>(n_rows) * O) ||
       !fits_int(static_cast<long long>(K) * O))
     return MOE_ERR_UNSUPPORTED;

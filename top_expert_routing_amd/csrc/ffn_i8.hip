@@ -145,9 +145,10 @@ __device__ __forceinline__ int wave_prefix(int v) {
 // over the lanes tells whose the block's is, and where per > 1 the lanes then take that
 // lane's groups one each.  The result is wave-uniform, in scalar registers.
 __device__ Item find_item(const ProductArgs& p, int BM, int nch) {
-  const int lane = lane_id(), x = blockIdx.x % kXcds;
+  const int block = blockIdx.y * kMostX + blockIdx.x;        // launch_of
+  const int lane = lane_id(), x = block % kXcds;
   const int per = (p.G + kWave - 1) / kWave;                // <= 64: at most 1280 groups
-  int slot = blockIdx.x / kXcds;
+  int slot = block / kXcds;
   GroupRows r{0, 0, 0, 0, 0, 0};
   int n = 0, g0 = 0;
   for (int i = 0; i < per; ++i) {
@@ -1016,7 +1017,8 @@ int device_cus() {
 
 template <Mode M, class Out>
 void launch_few(const ProductArgs& p, const Plan& plan, hipStream_t stream) {
-  const dim3 grid(plan.blocks), block(kThreadsS);
+  const Launch l = launch_of(plan);
+  const dim3 grid(l.x, l.y), block(kThreadsS);
   if (plan.width == 1) hipLaunchKernelGGL((few_i8<1, M, Out>), grid, block, 0, stream, p);
   else if (plan.width == 2) hipLaunchKernelGGL((few_i8<2, M, Out>), grid, block, 0, stream, p);
   else if constexpr (M != kGateUp) hipLaunchKernelGGL((few_i8<4, M, Out>), grid, block, 0, stream, p);
@@ -1032,7 +1034,8 @@ void launch_tile(const ProductArgs& p, hipStream_t stream) {
 template <Mode M, class Out>
 void launch_many(const ProductArgs& p, const Plan& plan, hipStream_t stream) {
   if (plan.kernel == Kernel::kStream) {
-    const dim3 grid(plan.blocks), block(kThreadsS);
+    const Launch l = launch_of(plan);
+    const dim3 grid(l.x, l.y), block(kThreadsS);
     if (plan.width == 1) hipLaunchKernelGGL((stream_i8<1, M, Out>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((stream_i8<2, M, Out>), grid, block, 0, stream, p);
   } else if (plan.kernel == Kernel::kTileWide) {

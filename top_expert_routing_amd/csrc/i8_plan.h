@@ -110,6 +110,16 @@ struct Plan {
   int blocks;   // few_i8, stream_i8: blocks of the launch (tile_i8's walk a list)
 };
 
+// The launch of a plan's blocks: those past 2^20 lie along y, because a grid has fewer than 2^32
+// threads along x (2^20 is a multiple of the XCDs, so block y * kMostX + x goes to XCD x % 8 as ever).
+constexpr int kMostX = 1 << 20;
+struct Launch {
+  int x, y;
+};
+inline Launch launch_of(const Plan& p) {
+  return p.blocks <= kMostX ? Launch{p.blocks, 1} : Launch{kMostX, (p.blocks - 1) / kMostX + 1};
+}
+
 inline Plan plan_few(Mode m, const Sizes& s) {
   const int tiles = max_m_tiles(s, 16), blocks16 = tiles * (s.cols / 16);
   // wider items where 16 columns give more blocks than run at once (a block is mostly waits:
