@@ -10,6 +10,7 @@ import tempfile
 import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "top_expert_routing_amd", "csrc")
 SRC = os.path.join(HERE, "native", "i8_plan_query.cpp")
 
 

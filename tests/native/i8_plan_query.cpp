@@ -8,6 +8,13 @@
 
 using namespace moe::i8;
 
+// every layout that the kernels use: its static_asserts hold
+template struct moe::i8::TileLds<TileWide, kLinear>;
+template struct moe::i8::TileLds<TileWide, kGateUp>;
+template struct moe::i8::TileLds<TileWide, kDown>;
+template struct moe::i8::TileLds<TileHalf, kLinear>;
+template struct moe::i8::TileLds<TileHalf, kGateUp>;
+
 int main() {
   char product[16];
   Sizes s;

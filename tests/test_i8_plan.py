@@ -1,5 +1,8 @@
 """Which kernel an int8 product runs on, and how it is launched (CPU only)."""
 import itertools
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -87,3 +90,23 @@ def test_launches_stay_below_two_to_the_32_threads():
         assert x * y >= blocks and (y == 1 or x % 8 == 0), q
         over += blocks * 512 >= 2 ** 32
     assert over > 4                       # some need more than one row
+
+
+@pytest.mark.parametrize("steps,compiles", [(4, True), (3, False)])
+def test_tiles_are_longer_than_what_is_requested_ahead(tmp_path, steps, compiles):
+    """A K as short as the stages requested ahead would take a tile's last stages from the wrong rows: such a minimum
+    does not compile."""
+    csrc = tmp_path / "top_expert_routing_amd" / "csrc"
+    native = tmp_path / "tests" / "native"
+    csrc.mkdir(parents=True)
+    native.mkdir(parents=True)
+    shutil.copy(os.path.join(i8_plan.CSRC, "item_plan.h"), csrc)
+    text = open(os.path.join(i8_plan.CSRC, "i8_plan.h")).read()
+    assert "kTileMinK = 4 * kStep;" in text
+    (csrc / "i8_plan.h").write_text(text.replace("kTileMinK = 4 * kStep;", f"kTileMinK = {steps} * kStep;"))
+    shutil.copy(i8_plan.SRC, native)
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    r = subprocess.run([cxx, "-std=c++17", "-fsyntax-only", str(native / "i8_plan_query.cpp")], capture_output=True, text=True)
+    assert (r.returncode == 0) == compiles and (compiles or "requested ahead" in r.stderr)

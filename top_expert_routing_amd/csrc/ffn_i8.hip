@@ -758,7 +758,7 @@ __global__ __launch_bounds__(C::NT, C::BPC * C::NW / 4) void tile_i8(ProductArgs
   aim(cur, 0);
   turn();
 #pragma unroll 1
-  for (int s = 0; s < L::AHEAD; ++s) {                         // stages >= AHEAD (checked by the host)
+  for (int s = 0; s < L::AHEAD; ++s) {                         // stages > AHEAD (TileLds, kTileMinK)
     load_scales();
 #pragma unroll
     for (int i = 0; i < PER; ++i) load(i);

@@ -23,6 +23,7 @@ struct TileCfg {
   static_assert(ADMA >= 1 && ADMA <= 4 && BDMA >= 1, "DMA instructions per wave");
 };
 constexpr int kLdsPerCu = 160 * 1024;
+constexpr int kTileMinK = 4 * kStep;   // shortest K of tile_i8 (TileLds)
 template <class C, Mode M>
 struct TileLds {
   static constexpr int SUB = M == kDown ? 2 : 1;               // K steps per stage
@@ -34,6 +35,9 @@ struct TileLds {
   static constexpr int STAGES = (kLdsPerCu / C::BPC - (C::BPC == 2 ? 8 : 12) * 1024) / STAGE;
   static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
   static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
+  // The stages requested before a block's first product stop short of its first tile's last one: what
+  // follows it is the next tile's, whose sources are set when the first tile starts.
+  static_assert(kTileMinK / (kStep * SUB) > AHEAD, "a tile has more stages than are requested ahead");
   static constexpr int RING = STAGES * STAGE;
   static constexpr int LIST = RING;                            // row list of two tiles
   static constexpr int SA = LIST + 2 * ROWS;                   // row scales of two tiles
@@ -73,7 +77,6 @@ constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
 constexpr int kIdleLinear = 200, kIdleFfn = 256;
 constexpr int kTileMinAvg = 64;
 constexpr int tile_min_items(Mode m) { return m == kGateUp ? 512 : m == kDown ? 736 : 576; }
-constexpr int kTileMinK = 4 * kStep;   // as many steps as tile_i8 has in flight, and one
 constexpr int kWideMinAvg = 192, kWideMinTiles = 256;
 
 // Rows of stream_i8's tiles, 16 * mf: 16 for groups that mostly fit (64 groups, 2048 x 1024, with
