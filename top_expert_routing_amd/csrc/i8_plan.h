@@ -71,7 +71,7 @@ using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves
 //                           (128 wide tiles) 32 / 34, 8191 x 4096 (512) 75 / 70.
 // Averages are rows per sequence that tiles are cut from (Sizes::sequences), not per group: with
 // 64 priority tokens, 128 experts x 4, 2880 x 2880, by group / by sequence: 1024 tokens 985 / 746,
-// 3072 tokens 1333 / 887, 4096 tokens 1535 / 967, 4160 tokens 969 / 966, 6144 tokens 1214 / 1084;
+// 2560 tokens 1229 / 831, 4096 tokens 1535 / 967, 4160 tokens 969 / 966, 6144 tokens 1214 / 1084;
 // 64 experts x 8, 2048 x 1024: 256 tokens 136 / 109, 1024 tokens 211 / 152, 2048 tokens 212 / 181.
 constexpr int kFewItems = 160, kFewBlocks = 384, kFewBlocksMost = 1024;
 constexpr int kIdleLinear = 200, kIdleFfn = 256;
