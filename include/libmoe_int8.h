@@ -86,8 +86,11 @@ moe_status moe_grouped_linear_i8(const int8_t* xq, const float* x_scale, const i
  *     h = s_down * sum over the blocks b of sa[b] * (aq . W_down over b)  (fp32 over the
  *         blocks, exact int32 inside one), rounded once to bf16.
  * A block of the SwiGLU product whose scale is below 2^-126 counts as zeros.
- * silu uses the hardware's exponential and reciprocal (2 ulp each), and a code
- * whose quotient lies within 1e-4 of a border may be the neighbour.
+ * g, u, silu and the scales are fp32 steps (the hardware's exponential and
+ * reciprocal among them), so a code whose exact quotient lies within
+ *     2^-16 * (22 + 2.2 * (n + m)) codes,  n = max(0, -g), m the largest n of the block,
+ * of a border may be the neighbour (measured: 1.4e-4 near g = -20, 3.2e-4 near
+ * -55), and a value of g below -87 may count as 0.
  *
  *   x_sorted, x_rows, n_x, group_offsets, n_rows, E, n_shared, nseg, h_sorted: as
  *                  moe_grouped_ffn with dtype MOE_BF16.  All n_x token rows are

@@ -63,9 +63,10 @@ __device__ __forceinline__ i32x4 mfma_i8(const uint4& w, const uint4& x, const i
 }
 
 // Scale of a block of the SwiGLU product and the factor of its codes.  The products carry
-// errors of a few 2^-23 anyhow, so their codes are rounded from v * (1 / scale) without
-// the exact quotient's correction: a code moves only where the quotient lies within
-// 1e-4 of a border.
+// relative errors of b = (9.2 + 2.2 max(0, -g)) * 2^-23 anyhow (silu_mul), and so does the
+// scale, their largest one / 127; so codes are rounded from v * (1 / scale) without the exact
+// quotient's correction, which adds 3.5 * 2^-23.  A code moves only where its quotient lies within
+// 127 times the sum of the three of a border (2^-16 * (22 + 2.2 * (n + m)) codes, libmoe_int8.h).
 struct BlockScale {
   float scale, r;
 };
@@ -101,8 +102,10 @@ __device__ __forceinline__ void transpose_rows(uint32_t (&d)[4]) {
   swap16(d[2], d[3]);
 }
 
-// silu(g) * u; the hardware's exponential and reciprocal are within 2 ulp, far below
-// half a code of the quantisation that follows
+// silu(g) * u.  In half steps of 2^-24: g and u arrive within 3 each; exp(-g) is within
+// 3 |g| (of g) + 1.3 |g| (the rounded argument of the exponential and its constant) + 4 (2 ulp), which
+// counts in full where g is far below zero and by at most |g| e^-g / (1 + e^-g) < 0.28 above; the sum,
+// the reciprocal (2 ulp) and the two products add 7.  Below g = -87 the reciprocal can flush to 0.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
