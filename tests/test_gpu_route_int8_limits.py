@@ -108,3 +108,19 @@ def test_linear_more_blocks_than_one_row_of_a_launch():
         assert bool(((y[e].double() - ref).abs() <= tol * ref.abs()).all()), e
     del w, ws, y
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ the layer
+def test_layer_refuses_tokens_its_raw_calls_would_read_wrongly():
+    """bound_calls hands out addresses: fp32 tokens, too few of them, or of another width would be read out of range."""
+    z = lambda *s, dt=torch.int8: torch.zeros(s, dtype=dt, device=DEV)
+    f, b = torch.float32, torch.bfloat16
+    E, k, d, I, T = 4, 2, 64, 128, 5
+    q = (z(E, I, d), z(E, I, dt=f), z(E, I, d), z(E, I, dt=f), z(E, d, I), z(E, d, dt=f))
+    for fused in (True, False):
+        layer = moe.MoeLayer(E, k, d, I, T, b, None, None, None, device=DEV, int8_weights=q, fused_gather=fused)
+        l = z(T, E, dt=f)
+        layer.bound_calls(l, z(T, d, dt=b))
+        for x in (z(T, d, dt=f), z(T - 1, d, dt=b), z(T, d - 8, dt=b), z(T, 2 * d, dt=b)[:, ::2], z(T, d, dt=b).cpu()):
+            with pytest.raises((TypeError, ValueError)):
+                layer.bound_calls(l, x)

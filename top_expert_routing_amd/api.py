@@ -989,6 +989,8 @@ class MoeLayer:
         offs = self.perm["group_offsets"].data_ptr()
         if self.int8_weights is not None:
             _need_i8_weights(self.h_sorted, self.E + self.S, self.d, self.I, self.int8_weights)
+            _out(x, "x", torch.bfloat16, (self.T, self.d))
+            _same_device(self.h_sorted, x=x)
             qg, sg, qu, su, qd, sd = (t.data_ptr() for t in self.int8_weights)
             return ("moe_grouped_ffn_i8", lib.moe_grouped_ffn_i8, (
                 src, rows, self.T, offs, self.N, self.E, self.S, self.nseg, self.d, self.I, qg, sg, qu, su, qd, sd,
