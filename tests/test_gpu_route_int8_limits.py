@@ -124,3 +124,136 @@ def test_layer_refuses_tokens_its_raw_calls_would_read_wrongly():
         for x in (z(T, d, dt=f), z(T - 1, d, dt=b), z(T, d - 8, dt=b), z(T, 2 * d, dt=b)[:, ::2], z(T, d, dt=b).cpu()):
             with pytest.raises((TypeError, ValueError)):
                 layer.bound_calls(l, x)
+
+
+# ------------------------------------------------------------------ empty calls and the largest ones
+def _i8(g, *shape):
+    return torch.randint(-127, 128, shape, generator=g, dtype=torch.int8)
+
+
+def test_empty_calls():
+    """No tokens, no sorted rows, or no rows in any group: nothing is read or written, with and without a row list."""
+    e = moe.route(torch.empty((0, 16), device=DEV), 2, "sigmoid", n_groups=4, top_groups=2)
+    assert e[0].shape == (0, 2) and e[1].shape == (0, 2)
+    g = _gen(23)
+    E, d, I = 3, 256, 256
+    w = [moe.pack_i8_codes(_i8(g, E, *s)).to(DEV) for s in ((I, d), (I, d), (d, I))]
+    s = [torch.ones((E, n), device=DEV) for n in (I, I, d)]
+    args = [t for pair in zip(w, s) for t in pair]
+    none = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    x, empty = torch.ones((7, d), dtype=torch.bfloat16, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV)
+    xq, xs = moe.quantize_rows_i8(x)
+    assert moe.grouped_linear_i8(xq, xs, none, E, 0, 1, w[0], s[0], x_rows=empty).shape == (0, I)
+    assert moe.grouped_linear_i8(xq[:0], xs[:0], none, E, 0, 1, w[0], s[0]).shape == (0, I)
+    assert moe.grouped_ffn_i8(x, none, E, 0, 1, *args, x_rows=empty).shape == (0, d)
+    assert moe.grouped_ffn_i8(x[:0], none, E, 0, 1, *args).shape == (0, d)
+    for rows, kernel in ((5, "few"), (400, "stream"), (40000, "tile_wide")):
+        assert i8_plan.ffn(rows, E, 0, 1, d, I)[0][0] == kernel
+        list_ = torch.zeros(rows, dtype=torch.int32, device=DEV)
+        for at in (0, rows):
+            offs = torch.full((E + 1,), at, dtype=torch.int32, device=DEV)
+            h = torch.full((rows, d), 3.0, dtype=torch.bfloat16, device=DEV)
+            moe.grouped_ffn_i8(x, offs, E, 0, 1, *args, h, x_rows=list_)
+            y = torch.full((rows, I), 3.0, device=DEV)
+            moe.grouped_linear_i8(xq, xs, offs, E, 0, 1, w[0], s[0], y, x_rows=list_)
+            assert bool((h == 3).all()) and bool((y == 3).all())
+
+
+def _linear_rows(xq, xs, w, ws, rows):
+    """y of some rows of a plain linear map, from exact integer sums (64-bit)."""
+    return (xq[rows].double().cpu() @ w[0].double().T) * xs[rows].double().cpu()[:, None] * ws[0].double()
+
+
+@pytest.mark.parametrize("rows,K,kernel", [(2 ** 24, 64, "stream"), (2 ** 23 - 64, 192, "stream"), (2 ** 23 - 64, 256, "tile_wide")])
+def test_linear_largest_row_counts(rows, K, kernel):
+    """As many sorted rows as a call takes; codes whose offsets come next to 2^31."""
+    announce(f"linear {rows} rows x {K}")
+    O = 64
+    assert rows * K < 2 ** 31 and i8_plan.linear(rows, 1, 0, 1, K, O)[0] == kernel
+    g = _gen(24)
+    some = _i8(g, 65537, K).to(DEV)
+    xq = some.repeat(rows // 65537 + 1, 1)[:rows].contiguous()
+    xs = (torch.arange(rows, device=DEV) % 251 + 1).float()
+    w, ws = _i8(g, 1, O, K), torch.rand((1, O), generator=g) + 0.5
+    offs = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    y = moe.grouped_linear_i8(xq, xs, offs, 1, 0, 1, moe.pack_i8_codes(w).to(DEV), ws.to(DEV))
+    pick = torch.cat([torch.arange(300), torch.arange(rows - 700, rows), torch.randint(0, rows, (4000,), generator=g)])
+    ref = _linear_rows(xq, xs, w, ws, pick.to(DEV))
+    tol = (3 * 2.0 ** -24 + torch.finfo(torch.bfloat16).eps / 2) * (1 + 1e-6)
+    assert bool(((y[pick.to(DEV)].double().cpu() - ref).abs() <= tol * ref.abs()).all())
+    # every other row: the same codes, so the same sums; scales are whole numbers
+    unit = moe.grouped_linear_i8(xq, torch.ones_like(xs), offs, 1, 0, 1, moe.pack_i8_codes(w).to(DEV), ws.to(DEV), out_dtype=torch.float32)
+    whole = rows // 65537 * 65537
+    assert torch.equal(unit[:whole].view(-1, 65537, O), unit[:65537].expand(rows // 65537, -1, -1))
+
+
+@pytest.mark.parametrize("rows,kernel", [(60, "few"), (3000, "stream"), (140000, "tile_wide")])
+def test_linear_row_lists_into_the_longest_codes(rows, kernel):
+    """Tokens whose codes end next to 2^31, read through a row list."""
+    n_x, K, O = 2 ** 23 - 1, 256, 128
+    announce(f"linear {rows} of {n_x} tokens")
+    assert i8_plan.linear(rows, 1, 0, 1, K, O)[0] == kernel
+    g = _gen(25)
+    xq = _i8(g, 4097, K).to(DEV).repeat(n_x // 4097 + 1, 1)[:n_x].contiguous()
+    xs = (torch.arange(n_x, device=DEV) % 13 + 1).float()
+    w, ws = _i8(g, 1, O, K), torch.rand((1, O), generator=g) + 0.5
+    list_ = torch.cat([n_x - 1 - torch.arange(rows // 2), torch.randint(0, n_x, (rows - rows // 2,), generator=g)])
+    y = moe.grouped_linear_i8(xq, xs, torch.tensor([0, rows], dtype=torch.int32, device=DEV), 1, 0, 1, moe.pack_i8_codes(w).to(DEV),
+                              ws.to(DEV), x_rows=list_.to(DEV, torch.int32), out_dtype=torch.float32)
+    ref = _linear_rows(xq, xs, w, ws, list_.to(DEV))
+    assert bool(((y.double().cpu() - ref).abs() <= 3 * 2.0 ** -24 * (1 + 1e-6) * ref.abs()).all())
+
+
+def test_ffn_largest_row_count():
+    """2^23 - 64 sorted rows of 700 tokens: each is what the same token gives in a batch of 70000."""
+    rows, d, I = 2 ** 23 - 64, 256, 256
+    announce(f"ffn {rows} rows")
+    g = _gen(26)
+    x = torch.randn((700, d), generator=g).bfloat16().to(DEV)
+    args = [t for s in ((I, d), (I, d), (d, I)) for t in (moe.pack_i8_codes(_i8(g, 1, *s)).to(DEV), torch.full((1, s[0]), 2e-3, device=DEV))]
+    assert {p[0] for n in (rows, 70000) for p in i8_plan.ffn(n, 1, 0, 1, d, I)} == {"tile_wide"}
+    run = lambda n: moe.grouped_ffn_i8(x, torch.tensor([0, n], dtype=torch.int32, device=DEV), 1, 0, 1, *args,
+                                       x_rows=torch.arange(n, dtype=torch.int32, device=DEV) % 700)
+    small = run(70000)[:700]
+    assert bool((small != 0).any(1).all())
+    h = run(rows)
+    whole = rows // 700 * 700
+    assert torch.equal(h[:whole].view(-1, 700, d), small.expand(rows // 700, -1, -1)) and torch.equal(h[whole:], small[:rows - whole])
+
+
+# ------------------------------------------------------------------ graphs, streams
+@pytest.mark.parametrize("rows,kernels", [(40, ["few", "few"]), (1500, ["stream", "stream"]), (20000, ["tile_half", "stream"]),
+                                          (90000, ["tile_wide", "tile_wide"])])
+def test_ffn_graphs_and_two_streams_on_each_kernel(rows, kernels):
+    """Captured and replayed with new tokens, between eager work, and twice at once with workspaces of their own."""
+    announce(f"ffn graph {rows} {kernels}")
+    E, d, I, T = 2, 256, 256, 500
+    assert [p[0] for p in i8_plan.ffn(rows, E, 0, 1, d, I)] == kernels
+    g = _gen(27)
+    args = [t for s in ((I, d), (I, d), (d, I)) for t in (moe.pack_i8_codes(_i8(g, E, *s)).to(DEV), torch.full((E, s[0]), 2e-3, device=DEV))]
+    offs = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device=DEV)
+    list_ = torch.randint(0, T, (rows,), generator=g, dtype=torch.int32).to(DEV)
+    x = torch.randn((T, d), generator=g).bfloat16().to(DEV)
+    h = torch.zeros((rows, d), dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(moe.ffn_i8_workspace_bytes(rows, T, d, I, E), dtype=torch.uint8, device=DEV)
+    eager = lambda: moe.grouped_ffn_i8(x, offs, E, 0, 1, *args, x_rows=list_)
+    step = lambda: moe.grouped_ffn_i8(x, offs, E, 0, 1, *args, h, ws, x_rows=list_)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        x.copy_(torch.randn((T, d), generator=g).bfloat16())
+        h.zero_()
+        ws.random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, eager())
+    outs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for s in streams * 2:
+        with torch.cuda.stream(s):
+            outs.append(eager())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, h) for o in outs)
