@@ -563,14 +563,15 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_i8(ProductArgs
 //   * what the epilogue and the next tile need from memory (the row list, the rows' and
 //     the channels' scales) comes by DMA too, a tile ahead, because a load that the
 //     compiler sees would make it wait for everything in flight.
-// Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave,
+// Waves: WM x WN, each MI x NJ blocks of 16x16 (TileCfg, TileLds: i8_plan.h); the 16-row blocks of the waves interleave,
 // so the rows of a partial tile spread over them.
 // 8191 x 2048 -> 4096 (fp32 out) takes 79 us, 1.74 POP/s; K = 8192 reaches 2.5.  The matrix
 // cores are busy 43 % of the cycles, waves wait 41 %: the barrier of each 64-wide step, the
 // first loads and the epilogue of a tile (some 7 us of 35) bound it.  An FFN of 4096 tokens x 8
 // of 128 experts, 2048 x 768, 266 us: a fifth of it are the experts' weights coming from HBM
 // (every tile on one expert's: 0.83 of the time), the rest ragged tiles and, in kDown, the
-// conversion and fma for each product.  Not kept: waves of 128 x 128, sixteen waves, panels of
+// conversion and fma for each product.  TileHalf (three stages) and kDown (two) wait for every load
+// in flight before a step, so that cold weights show as the rest of an HBM access.  Not kept: waves of 128 x 128, sixteen waves, panels of
 // 2 or 8 column chunks, tiles of equal height within a group, skipping the operand reads of
 // empty blocks, one barrier for two steps (it has to wait for every load and read: 81 us and
 // 278); each within 2 % or slower.

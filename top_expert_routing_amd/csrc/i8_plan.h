@@ -51,7 +51,8 @@ using TileWide = TileCfg<4, 8, 4, 2, 1>;   // 256 rows, one block of eight waves
 using TileHalf = TileCfg<4, 8, 2, 2, 2>;   // 128 rows, two blocks of four waves per CU
 
 // ---- which kernel ----------------------------------------------------------------------
-// The host sees the average group, not the groups.  Times of the whole call,
+// The host sees the average group, not the groups; items are counted against the MI355X's 256
+// CUs.  Times of the whole call,
 // us; d, I or K, O = 2048, 1024 (FFN, 64 groups) and 2048, 2048 (linear, one group).
 //   few_i8 or stream_i8     linear 16 rows 4.8 / 6.7, 128 rows 6.1 / 6.8, 256 rows 9.9 /
 //                           7.2: few_i8 up to kFewBlocksMost items of 16 x 16 (1024 x 512,

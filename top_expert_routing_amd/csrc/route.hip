@@ -4,8 +4,8 @@
 // byte run of the row).
 //
 // Bound by the vector instructions: a token of 256 experts in 8 groups with a bias
-// (k = 8, sigmoid) issues 625 and 227 scalar ones, so 8192 tokens, eight wavefronts a
-// SIMD, need 8.3 us of the 10.8 measured; 16 tokens take 4.3 us, most of it the launch.
+// (k = 8, sigmoid) issues 642 and 238 scalar ones, so 8192 tokens, eight wavefronts a
+// SIMD, need 8.5 us of the 11.0 measured; 16 tokens take 4.3 us, most of it the launch.
 //   * Everything that decides an id is computed in double, so that neighbouring
 //     scores fall as the definition says; fp64 runs at the fp32 rate here, and a
 //     score (an exponential and a division) costs about 45 instructions a lane.
@@ -16,7 +16,7 @@
 //     maximum retire it and leave its rank in the key's place, so nothing is moved to
 //     other lanes; each lane stores its chosen experts itself.  (Rounds that keep their
 //     winner in lane r and gather its score afterwards: 12.9 us and, bf16, 4159 tokens of
-//     160 experts, 11.0; now 8.8.)
+//     160 experts, 11.0; now 8.7.)
 //   * P is the smallest one that fits whose groups cover whole, power-of-two runs
 //     of lanes (8 groups of 32 experts: P = 4, 8 lanes a group; 8 of 20: P = 5,
 //     4 lanes): the groups' values then come from the same DPP steps.  Other
