@@ -9,6 +9,7 @@
 // one chain.)  Rows of more than 256 * 8 * kMaxHeld values are read twice.
 #include "launch.h"
 #include "quantize.h"
+#include "row_piece.h"
 
 namespace moe {
 
@@ -16,29 +17,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxHeld = 8;     // 8-value pieces of a row a lane holds
-
-struct Piece {
-  float v[8];
-};
-
-template <bool BF16>
-__device__ __forceinline__ Piece load8(const void* x, size_t i) {
-  Piece p;
-  if constexpr (BF16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      p.v[2 * j] = __uint_as_float(w[j] << 16);
-      p.v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + i + 4);
-    p = Piece{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-  }
-  return p;
-}
 
 __device__ __forceinline__ uint32_t piece_max(const Piece& p) {
   uint32_t m = 0;
