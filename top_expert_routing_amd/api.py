@@ -481,8 +481,8 @@ def quantize_fp8_rows(w: torch.Tensor):
 
 
 def pack_fp8_codes(q: torch.Tensor) -> torch.Tensor:
-    """E4M3 code matrices [..][R][K] (uint8) in the layout
-    moe_grouped_ffn_fp8w_packed reads: blocks of 16 rows x 64 codes, block
+    """E4M3 code matrices [..][R][K] (uint8 or float8_e4m3fn) in the layout
+    moe_grouped_ffn_fp8w_packed and the FP8 products read: blocks of 16 rows x 64 codes, block
     (r/16, k/64) at byte ((r/16) * (K/64) + k/64) * 1024 of each matrix and
     C[r][k] at (((k%64)/16) * 16 + r%16) * 16 + k%16 inside it; same shape."""
     *lead, R, K = q.shape
@@ -676,6 +676,207 @@ def grouped_ffn_i8(x: torch.Tensor, group_offsets: torch.Tensor, E: int, n_share
           group_offsets.data_ptr(), N, E, n_shared, nseg, d, I, w_gate.data_ptr(), s_gate.data_ptr(), w_up.data_ptr(),
           s_up.data_ptr(), w_down.data_ptr(), s_down.data_ptr(), h_sorted.data_ptr(), workspace.data_ptr(),
           ctypes.byref(nbytes))
+    return h_sorted
+
+
+FP8_BLOCK = 128       # columns of a row, and rows and columns of a matrix, that share a scale (MOE_FP8_BLOCK)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _code_out(q, s, rows, d, codes, like, index):
+    """Codes [*rows][d] and scales of a quantising call: the caller's, checked, or new ones."""
+    shape, dtype = (*rows, d), torch.float8_e4m3fn if codes == "fp8" else torch.int8
+    scales = (*rows, _blocks(d)) if codes == "fp8" else tuple(rows)
+    if q is None:
+        q = torch.empty(shape, dtype=dtype, device=index)
+    elif not _ok(q, index, dtype, shape):
+        _out(q, "q", dtype, shape)
+        _same_device(like, q=q)
+    if s is None:
+        s = torch.empty(scales, dtype=torch.float32, device=index)
+    elif not _ok(s, index, torch.float32, scales):
+        _out(s, "s", torch.float32, scales)
+        _same_device(like, s=s)
+    return q, s
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+            residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, codes: Optional[str] = None,
+            q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None, want_y: bool = True):
+    """Root-mean-square norm of the rows of x [..][d] times `weight` [d], the residual added first
+    (moe_rmsnorm).  Returns (y, q, s), None where not asked for.
+
+    residual: [..][d] bf16 or fp32; the sum goes to `residual_out` (`residual` itself, if not given) and the
+    norm is taken of it as stored there.  y has its own type or, if not given, x's; want_y=False leaves it
+    out.  codes: None, "i8" (int8 codes and a scale per row, for grouped_linear_i8) or "fp8" (E4M3 codes and
+    a scale for each 128 columns, for grouped_linear_fp8 and grouped_ffn_fp8)."""
+    _need(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dim")
+    if codes not in _lib.CODES:
+        raise ValueError('codes must be None, "i8" or "fp8"')
+    if not want_y and (codes is None or y is not None):
+        raise ValueError("want_y=False goes with codes and without y")
+    if codes is None and (q is not None or s is not None):
+        raise ValueError("q and s go with codes")
+    index, shape = x.get_device(), x.shape
+    *rows, d = shape
+    if not _ok(weight, index, weight.dtype, (d,)):
+        _out(weight, "weight", weight.dtype, (d,))
+        _same_device(x, weight=weight)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out goes with residual")
+    else:
+        if residual_out is None:
+            residual_out = residual
+        for name, t in (("residual", residual), ("residual_out", residual_out)):
+            if not _ok(t, index, residual.dtype, shape):
+                _out(t, name, residual.dtype, shape)
+                _same_device(x, **{name: t})
+    if y is None:
+        if want_y:
+            y = torch.empty(shape, dtype=x.dtype, device=index)
+    elif not _ok(y, index, y.dtype, shape):
+        _out(y, "y", y.dtype, shape)
+        _same_device(x, y=y)
+    T = x.numel() // d if d else 0
+    if codes is not None:
+        q, s = _code_out(q, s, rows, d, codes, x, index)
+    _call("moe_rmsnorm", index, _lib.load().moe_rmsnorm, x.data_ptr(), _dtype_code(x), _ptr(residual),
+          0 if residual is None else _dtype_code(residual), weight.data_ptr(), _dtype_code(weight), T, d, eps,
+          _ptr(residual_out), _ptr(y), 0 if y is None else _dtype_code(y), _lib.CODES[codes], _ptr(q), _ptr(s))
+    return y, q, s
+
+
+def quantize_blocks_fp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None):
+    """E4M3 codes [..][d] and fp32 scales [..][ceil(d / 128)] of the rows of x [..][d] (bf16 or fp32), a scale
+    for each 128 columns: max|block| * fl(1/448), codes to the nearest (moe_quantize_blocks_fp8)."""
+    _need(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dim")
+    index = x.get_device()
+    *rows, d = x.shape
+    q, s = _code_out(q, s, rows, d, "fp8", x, index)
+    _call("moe_quantize_blocks_fp8", index, _lib.load().moe_quantize_blocks_fp8, x.data_ptr(), _dtype_code(x),
+          x.numel() // d if d else 0, d, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def quantize_fp8_blocks(w: torch.Tensor):
+    """E4M3 quantisation of [..][R][K] weights with a scale for each 128 x 128 block (the last ones may be
+    smaller): scale = max|block| * fl(1/448) (1 where that is below 2^-100), codes = w / scale to the nearest.
+    Input preparation for the FP8 products, like quantize_fp8_rows; returns (codes float8_e4m3fn [..][R][K],
+    scales fp32 [..][ceil(R / 128)][ceil(K / 128)])."""
+    *lead, R, K = w.shape
+    rb, kb = _blocks(R), _blocks(K)
+    wf = w.float()
+    p = torch.nn.functional.pad(wf, (0, kb * FP8_BLOCK - K, 0, rb * FP8_BLOCK - R))
+    s = p.reshape(*lead, rb, FP8_BLOCK, kb, FP8_BLOCK).abs().amax(dim=(-3, -1)) * (1.0 / 448.0)
+    s = torch.where(s < 2.0 ** -100, torch.ones_like(s), s)
+    wide = s.repeat_interleave(FP8_BLOCK, -2).repeat_interleave(FP8_BLOCK, -1)[..., :R, :K]
+    return (wf / wide).to(torch.float8_e4m3fn).contiguous(), s.contiguous()
+
+
+def _need_fp8_rows(xq: torch.Tensor, x_scale: torch.Tensor, index: int) -> None:
+    scales = (xq.size(0), _blocks(xq.size(1)))
+    if not _ok(x_scale, index, torch.float32, scales):
+        _out(x_scale, "x_scale", torch.float32, scales)
+        _same_device(xq, x_scale=x_scale)
+
+
+def grouped_linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, group_offsets: torch.Tensor, E: int, n_shared: int,
+                       nseg: int, w: torch.Tensor, w_scale: torch.Tensor, y: Optional[torch.Tensor] = None,
+                       x_rows: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y[n] = xq . w[expert of row n] over blocks of 128 columns, each times its row's and its matrix's scale:
+    E4M3 rows [n_x][K] with x_scale [n_x][ceil(K/128)], packed E4M3 matrices [E+S][O][K] (quantize_fp8_blocks,
+    pack_fp8_codes) with w_scale [E+S][ceil(O/128)][ceil(K/128)]; bf16 or fp32 out (y's dtype, or `out_dtype`).
+    E = 1 with offsets [0, N] is a plain linear map (moe_grouped_linear_fp8)."""
+    f8 = torch.float8_e4m3fn
+    _need(xq, "xq", f8, 2)
+    if w.dim() != 3:
+        _need(w, "w", f8, 3)
+    n_x, K = xq.shape
+    G, O = E + n_shared, w.size(1)
+    index = xq.get_device()
+    N = _i8_batch(xq, x_rows, group_offsets, E, n_shared, nseg)
+    _need_fp8_rows(xq, x_scale, index)
+    if not (_ok(w, index, f8, (G, O, K)) and _ok(w_scale, index, torch.float32, (G, _blocks(O), _blocks(K)))):
+        _out(w, "w", f8, (G, O, K))
+        _out(w_scale, "w_scale", torch.float32, (G, _blocks(O), _blocks(K)))
+        _same_device(xq, w=w, w_scale=w_scale)
+    if y is None:
+        y = _new(N, O, out_dtype, index)
+    elif not _ok(y, index, y.dtype, (N, O)):
+        _out(y, "y", y.dtype, (N, O))
+        _same_device(xq, y=y)
+    _call("moe_grouped_linear_fp8", index, _lib.load().moe_grouped_linear_fp8, xq.data_ptr(), x_scale.data_ptr(),
+          _ptr(x_rows), n_x, group_offsets.data_ptr(), N, E, n_shared, nseg, K, O, w.data_ptr(), w_scale.data_ptr(),
+          _dtype_code(y), y.data_ptr())
+    return y
+
+
+def ffn_fp8_workspace_bytes(n_rows, I, E=1, n_shared=0, nseg=1, d=64) -> int:
+    """Workspace of grouped_ffn_fp8: the SwiGLU product's codes and their block scales."""
+    lib = _lib.load()
+    n = ctypes.c_size_t(0)
+    check("moe_grouped_ffn_fp8", lib.moe_grouped_ffn_fp8(None, None, None, 0, None, n_rows, E, n_shared, nseg, d, I, None,
+                                                         None, None, None, None, None, None, None, ctypes.byref(n),
+                                                         None))
+    return int(n.value)
+
+
+def _need_fp8_weights(like: torch.Tensor, G: int, d: int, I: int, weights) -> None:
+    """The six tensors (codes, block scales of gate, up, down) of an FP8 FFN over G experts."""
+    if len(weights) != 6:
+        raise ValueError("FP8 weights are codes and block scales of gate, up and down")
+    index, f8, f32 = like.get_device(), torch.float8_e4m3fn, torch.float32
+    ins, outs = (G, _blocks(I), _blocks(d)), (G, _blocks(d), _blocks(I))
+    w_gate, s_gate, w_up, s_up, w_down, s_down = weights
+    if (_ok(w_gate, index, f8, (G, I, d)) and _ok(w_up, index, f8, (G, I, d)) and _ok(w_down, index, f8, (G, d, I)) and
+            _ok(s_gate, index, f32, ins) and _ok(s_up, index, f32, ins) and _ok(s_down, index, f32, outs)):
+        return
+    for t, name, dtype, shape in ((w_gate, "w_gate", f8, (G, I, d)), (s_gate, "s_gate", f32, ins),
+                                  (w_up, "w_up", f8, (G, I, d)), (s_up, "s_up", f32, ins),
+                                  (w_down, "w_down", f8, (G, d, I)), (s_down, "s_down", f32, outs)):
+        _out(t, name, dtype, shape)
+        _same_device(like, **{name: t})
+
+
+def grouped_ffn_fp8(xq: torch.Tensor, x_scale: torch.Tensor, group_offsets: torch.Tensor, E: int, n_shared: int,
+                    nseg: int, w_gate: torch.Tensor, s_gate: torch.Tensor, w_up: torch.Tensor, s_up: torch.Tensor,
+                    w_down: torch.Tensor, s_down: torch.Tensor, h_sorted: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, x_rows: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The expert FFN on E4M3 rows [n_x][d] with x_scale [n_x][ceil(d/128)] (rmsnorm(codes="fp8") or
+    quantize_blocks_fp8) and packed E4M3 weights with 128 x 128 block scales (quantize_fp8_blocks,
+    pack_fp8_codes); rows read directly or through `x_rows`, bf16 out (moe_grouped_ffn_fp8)."""
+    _need(xq, "xq", torch.float8_e4m3fn, 2)
+    _need(w_gate, "w_gate", torch.float8_e4m3fn, 3)
+    n_x, d = xq.shape
+    I = w_gate.size(1)
+    index = xq.get_device()
+    N = _i8_batch(xq, x_rows, group_offsets, E, n_shared, nseg)
+    _need_fp8_rows(xq, x_scale, index)
+    _need_fp8_weights(xq, E + n_shared, d, I, (w_gate, s_gate, w_up, s_up, w_down, s_down))
+    if h_sorted is None:
+        h_sorted = _new(N, d, torch.bfloat16, index)
+    elif not _ok(h_sorted, index, torch.bfloat16, (N, d)):
+        _out(h_sorted, "h_sorted", torch.bfloat16, (N, d))
+        _same_device(xq, h_sorted=h_sorted)
+    if workspace is None:
+        workspace = torch.empty(max(ffn_fp8_workspace_bytes(N, I, E, n_shared, nseg, d), 256), dtype=torch.uint8,
+                                device=index)
+    elif not _ok(workspace, index, torch.uint8, (workspace.numel(),)):
+        _out(workspace, "workspace", torch.uint8, (workspace.numel(),))
+        _same_device(xq, workspace=workspace)
+    nbytes = ctypes.c_size_t(workspace.numel())
+    _call("moe_grouped_ffn_fp8", index, _lib.load().moe_grouped_ffn_fp8, xq.data_ptr(), x_scale.data_ptr(), _ptr(x_rows),
+          n_x, group_offsets.data_ptr(), N, E, n_shared, nseg, d, I, w_gate.data_ptr(), s_gate.data_ptr(),
+          w_up.data_ptr(), s_up.data_ptr(), w_down.data_ptr(), s_down.data_ptr(), h_sorted.data_ptr(),
+          workspace.data_ptr(), ctypes.byref(nbytes))
     return h_sorted
 
 

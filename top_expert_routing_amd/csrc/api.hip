@@ -6,7 +6,9 @@
 #include <mutex>
 
 #include "libmoe.h"
+#include "libmoe_fp8.h"
 #include "libmoe_int8.h"
+#include "libmoe_norm.h"
 #include "libmoe_route.h"
 #include "launch.h"
 
@@ -40,6 +42,7 @@ moe_status scratch_address(void** out) {
 constexpr long long kIntMax = 0x7fffffffLL;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool fits_int(long long v) { return v >= 0 && v <= kIntMax; }
@@ -172,9 +175,127 @@ moe_status grouped_i8_sizes(int32_t n_rows, int32_t E, int32_t n_shared, int32_t
   return MOE_OK;
 }
 
+// Checks shared by the grouped FP8 calls.
+moe_status grouped_fp8_sizes(int32_t n_rows, int32_t E, int32_t n_shared, int32_t nseg, int32_t K, int32_t O) {
+  if (n_rows < 0 || E < 1 || n_shared < 0 || (nseg != 1 && nseg != 2) || K < 1 || O < 1) return MOE_ERR_INVALID_ARG;
+  if (E > MOE_MAX_EXPERTS || n_shared > MOE_MAX_SHARED) return MOE_ERR_UNSUPPORTED;
+  if (K % 64 != 0 || O % 64 != 0) return MOE_ERR_UNSUPPORTED;
+  if (n_rows > 1 << 24) return MOE_ERR_UNSUPPORTED;   // keeps a launch within 2^25 blocks
+  if (!fits_int(static_cast<long long>(n_rows) * K) || !fits_int(static_cast<long long>(n_rows) * O) ||
+      !fits_int(static_cast<long long>(K) * O))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool known_code(moe_code c) { return c == MOE_CODE_NONE || c == MOE_CODE_I8 || c == MOE_CODE_FP8; }
+
+static_assert(int(moe::kCodeNone) == MOE_CODE_NONE && int(moe::kCodeI8) == MOE_CODE_I8 && int(moe::kCodeFp8) == MOE_CODE_FP8,
+              "launch.h and libmoe_norm.h name the codes alike");
+
 }  // namespace
 
 extern "C" {
+
+moe_status moe_rmsnorm(const void* x, moe_dtype x_dtype, const void* residual, moe_dtype residual_dtype,
+                       const void* weight, moe_dtype weight_dtype, int32_t T, int32_t d, float eps,
+                       void* residual_out, void* y, moe_dtype y_dtype, moe_code code, void* q, float* s,
+                       hipStream_t stream) {
+  if (T < 0 || d < 1 || !(eps > 0.f) || !__builtin_isfinite(eps) || !known_code(code)) return MOE_ERR_INVALID_ARG;
+  if (!known_dtype(x_dtype) || !known_dtype(weight_dtype) || (residual && !known_dtype(residual_dtype)) ||
+      (y && !known_dtype(y_dtype)))
+    return MOE_ERR_UNSUPPORTED;
+  if (d % 8 != 0 || !fits_int(static_cast<long long>(T) * ((d + 127) / 128))) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight || (!y && code == MOE_CODE_NONE) || (residual == nullptr) != (residual_out == nullptr) ||
+      (code != MOE_CODE_NONE && (!q || !s)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (code != MOE_CODE_NONE && (!aligned8(q) || !aligned4(s))) return MOE_ERR_INVALID_ARG;
+  moe::NormArgs a;
+  a.T = T;
+  a.d = d;
+  a.x_bf16 = x_dtype == MOE_BF16 ? 1 : 0;
+  a.residual_bf16 = residual && residual_dtype == MOE_BF16 ? 1 : 0;
+  a.weight_bf16 = weight_dtype == MOE_BF16 ? 1 : 0;
+  a.y_bf16 = y && y_dtype == MOE_BF16 ? 1 : 0;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.code = static_cast<int>(code);
+  a.q = static_cast<uint8_t*>(q);
+  a.s = s;
+  a.eps = eps;
+  return hip_status(moe::launch_rmsnorm(a, stream));
+}
+
+moe_status moe_quantize_blocks_fp8(const void* x, moe_dtype dtype, int32_t T, int32_t d, void* q, float* s,
+                                   hipStream_t stream) {
+  if (T < 0 || d < 1) return MOE_ERR_INVALID_ARG;
+  if (!known_dtype(dtype) || d % 8 != 0 || !fits_int(static_cast<long long>(T) * ((d + 127) / 128)))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !s) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned4(s) || !aligned8(q)) return MOE_ERR_INVALID_ARG;
+  return hip_status(
+      moe::launch_quantize_blocks(x, dtype == MOE_BF16 ? 1 : 0, T, d, static_cast<uint8_t*>(q), s, stream));
+}
+
+moe_status moe_grouped_linear_fp8(const void* xq, const float* x_scale, const int32_t* x_rows, int32_t n_x,
+                                  const int32_t* group_offsets, int32_t n_rows, int32_t E, int32_t n_shared,
+                                  int32_t nseg, int32_t K, int32_t O, const void* w, const float* w_scale,
+                                  moe_dtype out_dtype, void* y, hipStream_t stream) {
+  const moe_status st = grouped_fp8_sizes(n_rows, E, n_shared, nseg, K, O);
+  if (st != MOE_OK) return st;
+  if (!known_dtype(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (n_rows == 0) return MOE_OK;
+  if (!xq || !x_scale || !group_offsets || !w || !w_scale || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned4(x_scale) || !aligned4(group_offsets) || !aligned16(w) || !aligned4(w_scale) ||
+      !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (x_rows && (!aligned4(x_rows) || n_x < 1)) return MOE_ERR_INVALID_ARG;
+  if (x_rows && !fits_int(static_cast<long long>(n_x) * K)) return MOE_ERR_UNSUPPORTED;
+  moe::GroupedFp8 g{x_rows, x_rows ? n_x : n_rows, group_offsets, n_rows, E, n_shared, nseg};
+  return hip_status(moe::launch_grouped_linear_fp8(g, static_cast<const uint8_t*>(xq), x_scale, K, O,
+                                                   static_cast<const uint8_t*>(w), w_scale,
+                                                   out_dtype == MOE_BF16 ? 1 : 0, y, stream));
+}
+
+moe_status moe_grouped_ffn_fp8(const void* xq, const float* x_scale, const int32_t* x_rows, int32_t n_x,
+                               const int32_t* group_offsets, int32_t n_rows, int32_t E, int32_t n_shared,
+                               int32_t nseg, int32_t d, int32_t I, const void* w_gate, const float* s_gate,
+                               const void* w_up, const float* s_up, const void* w_down, const float* s_down,
+                               void* h_sorted, void* workspace, size_t* workspace_bytes, hipStream_t stream) {
+  moe_status st = grouped_fp8_sizes(n_rows, E, n_shared, nseg, d, I);
+  if (st != MOE_OK) return st;
+  bool query;
+  st = workspace_check(workspace, workspace_bytes, moe::ffn_fp8_workspace_bytes(n_rows, I), &query);
+  if (st != MOE_OK || query) return st;
+  if (n_rows == 0) return MOE_OK;
+  if (!xq || !x_scale || !group_offsets || !w_gate || !w_up || !w_down || !s_gate || !s_up || !s_down || !h_sorted)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned4(x_scale) || !aligned4(group_offsets) || !aligned16(w_gate) || !aligned16(w_up) ||
+      !aligned16(w_down) || !aligned4(s_gate) || !aligned4(s_up) || !aligned4(s_down) || !aligned16(h_sorted))
+    return MOE_ERR_INVALID_ARG;
+  if (x_rows && (!aligned4(x_rows) || n_x < 1)) return MOE_ERR_INVALID_ARG;
+  if (x_rows && !fits_int(static_cast<long long>(n_x) * d)) return MOE_ERR_UNSUPPORTED;
+  moe::FfnFp8Args a;
+  a.g = moe::GroupedFp8{x_rows, x_rows ? n_x : n_rows, group_offsets, n_rows, E, n_shared, nseg};
+  a.xq = static_cast<const uint8_t*>(xq);
+  a.xs = x_scale;
+  a.d = d;
+  a.I = I;
+  a.w_gate = static_cast<const uint8_t*>(w_gate);
+  a.w_up = static_cast<const uint8_t*>(w_up);
+  a.w_down = static_cast<const uint8_t*>(w_down);
+  a.s_gate = s_gate;
+  a.s_up = s_up;
+  a.s_down = s_down;
+  a.h_sorted = h_sorted;
+  return hip_status(moe::launch_ffn_fp8(a, workspace, stream));
+}
 
 moe_status moe_route(const void* logits, moe_dtype dtype, const float* bias, int32_t T, int32_t E, int32_t k,
                      moe_score score, int32_t n_groups, int32_t top_groups, moe_group_rank group_rank,

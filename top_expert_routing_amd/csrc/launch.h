@@ -116,6 +116,43 @@ struct FfnI8Args {
 size_t ffn_i8_workspace_bytes(int n_rows, int n_tokens, int d, int I);
 hipError_t launch_ffn_i8(const FfnI8Args& a, void* workspace, hipStream_t stream);
 
+// ---- norm and FP8 block codes -----------------------------------------------------
+enum CodeKind { kCodeNone, kCodeI8, kCodeFp8 };
+struct NormArgs {
+  int T, d;
+  int x_bf16, residual_bf16, weight_bf16, y_bf16;   // 1 bf16, 0 fp32
+  const void *x, *residual, *weight;                // residual: nullptr for none
+  void *residual_out, *y;                           // y: nullptr for none
+  int code;                                         // CodeKind of q and s
+  uint8_t* q;
+  float* s;
+  float eps;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_quantize_blocks(const void* x, int bf16, int T, int d, uint8_t* q, float* s, hipStream_t stream);
+
+// ---- FP8 products -----------------------------------------------------------------
+struct GroupedFp8 {
+  const int* x_rows;   // nullptr: sorted row n reads row n
+  int n_x;
+  const int* group_offsets;
+  int n_rows, E, n_shared, nseg;
+};
+// y[n][o], packed E4M3 weights [E+S][O][K]; bf16: output type
+hipError_t launch_grouped_linear_fp8(const GroupedFp8& g, const uint8_t* xq, const float* xs, int K, int O,
+                                     const uint8_t* w, const float* ws, int bf16, void* y, hipStream_t stream);
+struct FfnFp8Args {
+  GroupedFp8 g;
+  const uint8_t* xq;
+  const float* xs;
+  int d, I;
+  const uint8_t *w_gate, *w_up, *w_down;
+  const float *s_gate, *s_up, *s_down;
+  void* h_sorted;
+};
+size_t ffn_fp8_workspace_bytes(int n_rows, int I);
+hipError_t launch_ffn_fp8(const FfnFp8Args& a, void* workspace, hipStream_t stream);
+
 // ---- combine ---------------------------------------------------------------
 hipError_t launch_combine(const void* h_sorted, const int* flat_to_sorted, const float* topk_w, int T,
                           int k, int n_shared, int d, int bf16, void* y, hipStream_t stream);

@@ -1,0 +1,240 @@
+// Root-mean-square norm of rows with the residual's addition in front of it and codes behind it
+// (moe_rmsnorm), and the quantiser to E4M3 codes (moe_quantize_blocks_fp8).
+//
+// The norm of a row r multiplies all of it by one number, rstd, so codes do not depend on it: they are
+// those of p = r * w, and rstd only multiplies their scale.  So one pass over the row in registers yields
+// the sum of squares and every maximum, and one exchange between the wavefronts joins them.
+// Bound by memory: x, residual, residual, y and codes are 2 + 2 + 2 + 2 + 1 bytes a value in bf16.
+// A block of four wavefronts takes a row, or, where a row has no more values than the loads of one
+// wavefront, each wavefront one.  Rows of more than 256 * 8 * kMaxHeld values are read twice.
+#include "fp8_block.h"
+#include "launch.h"
+#include "row_piece.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHeld = 8;     // 8-value pieces of a row a lane holds
+
+__device__ __forceinline__ uint32_t piece_max(const Piece& p) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(p.v[j]));
+  return m;
+}
+
+// LANES threads per row; HELD pieces each (0: the row is read again for its outputs).
+template <int LANES, int HELD>
+__global__ __launch_bounds__(kThreads) void rmsnorm(NormArgs a) {
+  constexpr int WAVES = LANES / kWave;
+  __shared__ float sums[kThreads / kWave];
+  __shared__ uint32_t tops[kThreads / kWave];
+  const int t = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES, l = threadIdx.x % LANES;
+  if (LANES == kWave && t >= a.T) return;       // one row per block otherwise
+  const int d = a.d, nb = (d + kFp8Block - 1) / kFp8Block;
+  const size_t row = static_cast<size_t>(t) * d;
+
+  // r of a piece at column i: x, or the sum as it is stored
+  auto add = [&](Piece& p, const Piece& r, uint32_t i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p.v[j] += r.v[j];
+    if (a.residual_bf16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p.v[j] = bf16_to_f32(f32_to_bf16(p.v[j]));
+    }
+    store8(a.residual_bf16, a.residual_out, row + i, p);
+  };
+  auto weigh = [&](Piece& p, uint32_t i) {
+    const Piece w = load8(a.weight_bf16, a.weight, i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p.v[j] *= w.v[j];
+  };
+  auto squares = [&](const Piece& p) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(p.v[j], p.v[j], s);
+    return s;
+  };
+
+  Piece held[HELD > 0 ? HELD : 1];              // p = r * w
+  float sum = 0.f;
+  uint32_t top = 0;
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      const int i = (h * LANES + l) * 8;
+      held[h] = Piece{};
+      if (i < d) held[h] = load8(a.x_bf16, a.x, row + i);
+    }
+    if (a.residual) {                           // all of it is asked for before the first sum is stored
+      Piece r[HELD];
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) {
+        const int i = (h * LANES + l) * 8;
+        if (i < d) r[h] = load8(a.residual_bf16, a.residual, row + i);
+      }
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) {
+        const int i = (h * LANES + l) * 8;
+        if (i < d) add(held[h], r[h], i);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      const int i = (h * LANES + l) * 8;
+      sum += squares(held[h]);
+      if (i < d) weigh(held[h], i);
+      if (a.code == kCodeI8) top = max(top, piece_max(held[h]));
+    }
+  } else {
+    // unsigned: the last step of a row next to 2^31 values passes int32
+    for (uint32_t i = l * 8; i < static_cast<uint32_t>(d); i += LANES * 8) {
+      Piece p = load8(a.x_bf16, a.x, row + i);
+      if (a.residual) add(p, load8(a.residual_bf16, a.residual, row + i), i);
+      sum += squares(p);
+      if (a.code == kCodeI8) {
+        weigh(p, i);
+        top = max(top, piece_max(p));
+      }
+    }
+  }
+  sum = wave_sum(sum);
+  if (a.code == kCodeI8) {
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o, kWave)));
+  }
+  if constexpr (WAVES > 1) {
+    if (lane_id() == 0) {
+      sums[threadIdx.x >> 6] = sum;
+      tops[threadIdx.x >> 6] = top;
+    }
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      sum += sums[w];
+      top = max(top, tops[w]);
+    }
+  }
+  // a row that is not finite, or whose sum of squares is not: NaN everywhere
+  const float mean = sum / static_cast<float>(d);
+  const float rstd = __builtin_isfinite(sum) ? 1.0f / __builtin_sqrtf(mean + a.eps) : __builtin_nanf("");
+  const QuantScale qs = quant_scale(top);
+
+  auto finish = [&](const Piece& p, int i, bool in) {          // every lane of the 16 that share a block takes part
+    if (a.y && in) {
+      Piece y;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y.v[j] = p.v[j] * rstd;
+      store8(a.y_bf16, a.y, row + i, y);
+    }
+    if (a.code == kCodeFp8) {
+      const Fp8Scale fs = fp8_scale(row16_max(piece_max(p)));
+      if (in) *reinterpret_cast<uint2*>(a.q + row + i) = fp8_codes8(p.v, fs);
+      if (in && i % kFp8Block == 0) a.s[static_cast<size_t>(t) * nb + i / kFp8Block] = fs.base * rstd;
+    } else if (a.code == kCodeI8 && in) {
+      *reinterpret_cast<uint2*>(a.q + row + i) = quant_codes8(p.v, qs);
+    }
+  };
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      const int i = (h * LANES + l) * 8;
+      finish(held[h], i, i < d);
+    }
+  } else {
+    for (uint32_t i0 = 0; i0 < static_cast<uint32_t>(d); i0 += LANES * 8) {
+      const uint32_t i = i0 + l * 8;
+      const bool in = i < static_cast<uint32_t>(d);
+      Piece p{};
+      if (in) {
+        p = a.residual ? load8(a.residual_bf16, a.residual_out, row + i) : load8(a.x_bf16, a.x, row + i);
+        weigh(p, i);
+      }
+      finish(p, static_cast<int>(i), in);
+    }
+  }
+  if (a.code == kCodeI8 && l == 0) a.s[t] = qs.scale * rstd;
+}
+
+void launch_norm_rows(const NormArgs& a, hipStream_t stream) {
+  const dim3 block(kThreads);
+  if (a.d <= kWave * 8) {
+    const dim3 grid((a.T + kThreads / kWave - 1) / (kThreads / kWave));
+    hipLaunchKernelGGL((rmsnorm<kWave, 1>), grid, block, 0, stream, a);
+    return;
+  }
+  const int pieces = (a.d / 8 + kThreads - 1) / kThreads;
+  const dim3 grid(a.T);
+  if (pieces <= 1) hipLaunchKernelGGL((rmsnorm<kThreads, 1>), grid, block, 0, stream, a);
+  else if (pieces <= 2) hipLaunchKernelGGL((rmsnorm<kThreads, 2>), grid, block, 0, stream, a);
+  else if (pieces <= 4) hipLaunchKernelGGL((rmsnorm<kThreads, 4>), grid, block, 0, stream, a);
+  else if (pieces <= kMaxHeld) hipLaunchKernelGGL((rmsnorm<kThreads, kMaxHeld>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((rmsnorm<kThreads, 0>), grid, block, 0, stream, a);
+}
+
+// ---- quantiser ------------------------------------------------------------------------
+// 16 lanes take the 128 columns of a block, eight values each; n blocks from block `first`, nb in a row.
+constexpr int kBlocksPer = kThreads / 16;
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void quantize_blocks(const void* __restrict__ x, int d, int nb, uint32_t first,
+                                                            uint32_t n, uint8_t* __restrict__ q, float* __restrict__ s) {
+  const uint32_t k = blockIdx.x * kBlocksPer + threadIdx.x / 16;
+  const uint32_t b = first + min(k, n - 1);
+  const uint32_t t = b / nb, i = (b - t * nb) * kFp8Block + threadIdx.x % 16 * 8;
+  const bool in = k < n && i < static_cast<uint32_t>(d);
+  const size_t at = static_cast<size_t>(t) * d + i;
+  Piece p{};
+  if (in) p = load8<BF16>(x, at);
+  const Fp8Scale fs = fp8_scale(row16_max(piece_max(p)));
+  if (!in) return;
+  *reinterpret_cast<uint2*>(q + at) = fp8_codes8(p.v, fs);
+  if (threadIdx.x % 16 == 0) s[b] = fs.base;
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t stream) {
+  // a grid has fewer than 2^32 threads: at most 2^23 rows of a block each in a launch
+  constexpr int kMost = 1 << 23;
+  const int nb = (args.d + kFp8Block - 1) / kFp8Block;
+  for (int t = 0; t < args.T; t += kMost) {
+    NormArgs a = args;
+    a.T = args.T - t < kMost ? args.T - t : kMost;
+    const size_t at = static_cast<size_t>(t) * args.d;
+    auto from = [&](const void* p, int bf16) { return p ? static_cast<const char*>(p) + at * (bf16 ? 2 : 4) : nullptr; };
+    a.x = from(args.x, a.x_bf16);
+    a.residual = from(args.residual, a.residual_bf16);
+    a.residual_out = const_cast<char*>(from(args.residual_out, a.residual_bf16));
+    a.y = const_cast<char*>(from(args.y, a.y_bf16));
+    if (a.code != kCodeNone) {
+      a.q = args.q + at;
+      a.s = args.s + static_cast<size_t>(t) * (a.code == kCodeFp8 ? nb : 1);
+    }
+    launch_norm_rows(a, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.T < kMost) break;                     // t + kMost may pass int32
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_quantize_blocks(const void* x, int bf16, int T, int d, uint8_t* q, float* s, hipStream_t stream) {
+  constexpr uint32_t kMost = 1u << 27;          // blocks of 128 columns in a launch: 2^23 blocks of threads
+  const int nb = (d + kFp8Block - 1) / kFp8Block;
+  const uint32_t all = static_cast<uint32_t>(T) * nb;          // in int32 (moe_quantize_blocks_fp8)
+  for (uint32_t b = 0; b < all; b += kMost) {
+    const uint32_t n = all - b < kMost ? all - b : kMost;
+    const dim3 grid((n + kBlocksPer - 1) / kBlocksPer), block(kThreads);
+    if (bf16) hipLaunchKernelGGL((quantize_blocks<true>), grid, block, 0, stream, x, d, nb, b, n, q, s);
+    else hipLaunchKernelGGL((quantize_blocks<false>), grid, block, 0, stream, x, d, nb, b, n, q, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe
