@@ -1,0 +1,31 @@
+// Prints the kernel that the library picks for FP8 products: one line
+// "product n_rows E n_shared nseg K cols" in (product: linear, linear_f32, gate_up, down), one line
+// "kernel width blocks x y" out (x, y: the launch's grid).
+#include <cstdio>
+#include <cstring>
+
+#include "../../top_expert_routing_amd/csrc/fp8_plan.h"
+
+using namespace moe::fp8;
+
+// every layout that the kernels use: its static_asserts hold
+template struct moe::fp8::TileLds<TileWide, kLinear>;
+template struct moe::fp8::TileLds<TileWide, kGateUp>;
+template struct moe::fp8::TileLds<TileWide, kDown>;
+template struct moe::fp8::TileLds<TileLow, kLinear>;
+template struct moe::fp8::TileLds<TileLow, kGateUp>;
+template struct moe::fp8::TileLds<TileLow, kDown>;
+template struct moe::fp8::TileLds<TileExact, kLinear>;
+
+int main() {
+  char product[16];
+  Sizes s;
+  while (std::scanf("%15s %d %d %d %d %d %d", product, &s.n_rows, &s.E, &s.n_shared, &s.nseg, &s.K, &s.cols) == 7) {
+    const Mode m = !std::strcmp(product, "gate_up") ? kGateUp : !std::strcmp(product, "down") ? kDown : kLinear;
+    const Plan p = plan(m, !std::strcmp(product, "linear_f32"), s);
+    const char* names[] = {"stream", "tile_low", "tile_wide", "tile_exact"};
+    const Launch l = launch_of(moe::i8::Plan{moe::i8::Kernel::kStream, p.width, p.blocks});
+    std::printf("%s %d %d %d %d\n", names[static_cast<int>(p.kernel)], p.width, p.blocks, l.x, l.y);
+  }
+  return 0;
+}

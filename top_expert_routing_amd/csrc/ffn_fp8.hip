@@ -22,7 +22,7 @@
 
 #include "common.h"
 #include "fp8_block.h"
-#include "i8_plan.h"
+#include "fp8_plan.h"
 #include "launch.h"
 #include "tile_util.h"
 
@@ -30,13 +30,12 @@ namespace moe {
 
 namespace {
 
-using i8::kDown;
-using i8::kGateUp;
-using i8::kLinear;
-using i8::Mode;
+using namespace fp8;
 
-constexpr int kBlock = kFp8Block;
-constexpr int kHalf = 64;                // columns of a packed block: half of what an instruction takes
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+static_assert(kBlock == kFp8Block && i8::kLanes == kWave, "one block size, one wavefront");
+constexpr int kMaxGroups = 2 * 512 + 256;
 
 struct ProductArgs {
   const uint8_t* a;        // codes of the rows: [n_x][K]
@@ -77,6 +76,14 @@ __device__ __forceinline__ f32x4 mfma_wide(const Wide& w, const Wide& x) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x.v[h], t, 0, 0, 0);
   return t;
+}
+
+// The same on the FP8 instructions: w and x are the two 16-byte pieces of each lane's columns.
+__device__ __forceinline__ f32x4 mfma_codes(const uint4 (&w)[2], const uint4 (&x)[2]) {
+  struct Two { uint4 v[2]; };
+  const i32x8 a = __builtin_bit_cast(i32x8, (Two{{w[0], w[1]}}));
+  const i32x8 b = __builtin_bit_cast(i32x8, (Two{{x[0], x[1]}}));
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
 // Codes of the SwiGLU product from v * (1 / scale) without the exact quotient's correction: the
@@ -250,16 +257,389 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_fp8(ProductArgs p) {
   }
 }
 
-i8::Sizes sizes_of(const ProductArgs& p) { return i8::Sizes{p.n_rows, p.E, p.G - p.nseg * p.E, p.nseg, p.K, p.cols}; }
+// ---- large groups: LDS-tiled products ----------------------------------------------
+// A persistent block (one per CU) walks its list of tiles: BM rows x BN weight rows
+// (kGateUp: 128 gate and the same 128 up rows).  K advances 128 codes a stage through a
+// ring of LDS stages that LDS-DMA loads fill ahead; the stages of all tiles form one
+// stream, so the next tile's first stages load while this one finishes.
+//   * rows: a stage holds them as two halves of 64 codes, four 16-byte pieces each; piece c of row
+//     r lies at slot c ^ swz(r), so that the 16 rows of an operand read hit different banks.  A DMA
+//     instruction fills 16 rows (lane -> row lane / 4, slot lane % 4).
+//   * weights: a packed block (16 rows x 64 codes, 1 KiB) is copied as it is.
+//   * scales: one 4-byte load per wave and stage, its rows' in lanes 0 - 31, the matrix's (kGateUp:
+//     gate's and up's, else those of the tile's two blocks of 128 columns) in lanes 32 and 33.
+//   * the row list comes by DMA too, a tile ahead, because a load that the compiler sees would
+//     make it wait for everything in flight.
+// Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave, so the
+// rows of a partial tile spread over them.
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+
+template <class C, Mode M, bool EXACT, class Out>
+__global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
+  using L = TileLds<C, M>;
+  constexpr int MI = C::MI, NJ = C::NJ, WM = C::WM, WN = C::WN, NW = C::NW, NT = C::NT, BM = C::BM;
+  constexpr int OUTC = M == kGateUp ? C::BN / 2 : C::BN;
+  constexpr int GPT = (kMaxGroups + NT - 1) / NT;
+  constexpr int kPanel = 4;                                    // column chunks that follow each other per m-tile
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  int* wsum = reinterpret_cast<int*>(lds + L::PLAN);
+  int* before = wsum + NW;                                     // m-tiles before group g
+  int* offs = before + p.G + 1;
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+  const int K = p.K, cols = p.cols;
+  const int nb = (K + kBlock - 1) / kBlock, ncb = (cols + kBlock - 1) / kBlock;
+
+  for (int g = tid; g <= p.G; g += NT) offs[g] = p.offs[g];
+  __syncthreads();
+  {
+    int cnt[GPT], sum = 0;
+#pragma unroll
+    for (int i = 0; i < GPT; ++i) {
+      const int g = tid * GPT + i;
+      cnt[i] = g < p.G ? group_rows(offs, p.n_rows, p.E, p.nseg, BM, g).nt : 0;
+      sum += cnt[i];
+    }
+    const int incl = wave_prefix(sum);
+    if (lane == kWave - 1) wsum[wave] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int i = 0; i < wave; ++i) run += wsum[i];
+#pragma unroll
+    for (int i = 0; i < GPT; ++i) {
+      const int g = tid * GPT + i;
+      if (g < p.G) before[g] = run;
+      run += cnt[i];
+    }
+    if (tid == NT - 1) before[p.G] = run;
+    __syncthreads();
+  }
+  // XCD x (blocks are dealt round-robin) owns the x-th eighth of the list of tiles, so
+  // that tiles which share weights or rows run in one L2; its blocks take them in turn
+  const int nch = (cols + OUTC - 1) / OUTC;
+  const int items = __builtin_amdgcn_readfirstlane(before[p.G]) * nch;
+  const int per_xcd = static_cast<int>(gridDim.x) / kXcds;
+  const int share = (items + kXcds - 1) / kXcds;
+  const int first = static_cast<int>(blockIdx.x % kXcds) * share + static_cast<int>(blockIdx.x / kXcds);
+  const int end = min(items, static_cast<int>(blockIdx.x % kXcds + 1) * share);
+  const int n_my = first < end ? (end - first - 1) / per_xcd + 1 : 0;
+  if (n_my == 0) return;
+  auto item_of = [&](int i) MOE_INLINE -> Item {
+    const int want = first + i * per_xcd;
+    const int u = want / nch;
+    int lo = 0, hi = p.G;                                      // last g with before[g] <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= u) lo = mid; else hi = mid;
+    }
+    const int nt = before[lo + 1] - before[lo];
+    const int local = want - before[lo] * nch;
+    const int panel = local / (kPanel * nt), rest = local - panel * kPanel * nt;
+    const int pc = min(kPanel, nch - panel * kPanel);
+    return uniform(group_tile(group_rows(offs, p.n_rows, p.E, p.nseg, BM, lo), lo, rest / pc, panel * kPanel + rest % pc,
+                              BM, p.E, p.nseg));
+  };
+
+  // ---- the loads, STAGES - 1 stages ahead of the products
+  const uint32_t lds0 = lds_address(lds);
+  const int halves = K / kHalf;
+  uint32_t ao[C::ADMA], ao_next[C::ADMA];                      // this lane's bytes from p.a: tile being loaded, tile after it
+  const uint8_t *bp[C::BDMA], *bp_next[C::BDMA];               // wave-uniform
+  const float *sp, *sp_next;                                   // this lane's scales, one per stage, sstep apart
+  // lane 16 i + r of a wave has row r of the 16 rows of its load i, so wave w's rows are the w-th 16 * ADMA of ROWS
+  const bool vlane = lane < 16 * C::ADMA, slane = vlane || (lane >> 1) == 16;
+  const int vrow = 16 * (wave + NW * (lane >> 4)) + l16;
+  const size_t sstep = lane < 32 ? p.as_block : 1;
+  auto load_list = [&](const Item& it, int parity) MOE_INLINE {
+    if (p.x_rows && vlane)
+      dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * L::WROWS);
+  };
+  // Sources of a tile whose row list has arrived.
+  auto aim = [&](const Item& it, int parity) MOE_INLINE {
+    const int* list = reinterpret_cast<const int*>(lds + L::LIST + parity * L::ROWS + wave * L::WROWS);
+    auto src = [&](int r, int slot) MOE_INLINE {
+      return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : it.row(min(r, it.rows - 1));
+    };
+#pragma unroll
+    for (int i = 0; i < C::ADMA; ++i) {
+      const int r = 16 * (wave + NW * i) + (lane >> 2);
+      ao_next[i] = static_cast<uint32_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
+    }
+    const int n0 = it.chunk * OUTC;
+    const size_t e0 = static_cast<size_t>(it.expert) * cols;
+#pragma unroll
+    for (int i = 0; i < C::BDMA; ++i) {
+      const int b = wave + NW * i;                             // 16-row block of the tile
+      const bool up = M == kGateUp && b >= C::BN / 32;
+      const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
+      bp_next[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
+    }
+    const int second = lane & 1;
+    const int cb = M == kGateUp ? it.chunk : min(it.chunk * (OUTC / kBlock) + second, ncb - 1);
+    const float* sw = (M == kGateUp && second ? p.s1 : p.s0) + (static_cast<size_t>(it.expert) * ncb + cb) * nb;
+    sp_next = vlane ? p.as + src(vrow, lane & (16 * C::ADMA - 1)) * p.as_row : sw;
+  };
+  int ikt = 0, islot = 0;                                      // the stage requested next: of its tile, ring slot
+  auto turn = [&]() MOE_INLINE {                               // go on with the next tile
+    ikt = 0;
+#pragma unroll
+    for (int i = 0; i < C::ADMA; ++i) ao[i] = ao_next[i];
+#pragma unroll
+    for (int i = 0; i < C::BDMA; ++i) bp[i] = bp_next[i];
+    sp = sp_next;
+  };
+  constexpr int CODES = 2 * (C::ADMA + C::BDMA);               // loads of a stage per wave: of codes,
+  constexpr int PER = CODES + 1;                               // and one of scales
+  auto load = [&](int i) MOE_INLINE {                          // the i-th of them
+    const uint32_t st = lds0 + islot * L::STAGE;
+    if (i == CODES) {
+      if (slane) dma4(sp + ikt * sstep, st + 2 * (L::A + L::B) + wave * L::WSCALES);
+      return;
+    }
+    const int h = i / (C::ADMA + C::BDMA), n = i % (C::ADMA + C::BDMA);
+    const int kt = min(2 * ikt + h, halves - 1);               // the half past K: the last one again (see a1 below)
+    if (n < C::ADMA) dma16(p.a + kt * kHalf, ao[n], st + h * L::A + (n * NW + wave) * 1024);
+    else dma16(bp[n - C::ADMA] + static_cast<size_t>(kt) * 1024, lane * 16,
+               st + 2 * L::A + h * L::B + ((n - C::ADMA) * NW + wave) * 1024);
+  };
+  auto loaded = [&]() MOE_INLINE {
+    islot = islot + 1 == L::STAGES ? 0 : islot + 1;
+    if (++ikt == nb) turn();
+  };
+  Item cur = item_of(0), nxt = n_my > 1 ? item_of(1) : cur;
+  load_list(cur, 0);
+  load_list(nxt, 1);
+  wait_loads_barrier<0>();
+  aim(cur, 0);
+  turn();
+#pragma unroll 1
+  for (int s = 0; s < L::AHEAD; ++s) {                         // nb > AHEAD (kTileMinStages)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) load(i);
+    loaded();
+  }
+
+  // ---- compute side
+  const int aoff = 16 * wm * kHalf + l16 * kHalf + 16 * (q ^ swz(l16));   // 16-row blocks do not change swz
+  int cslot = 0;
+  auto next_stage = [&]() MOE_INLINE {
+    const uint8_t* st = lds + cslot * L::STAGE;
+    cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
+    return st;
+  };
+  auto bfrag = [&](const uint8_t* st, int h, int j) MOE_INLINE {
+    const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2) : wn * NJ + j;
+    return *reinterpret_cast<const uint4*>(st + 2 * L::A + h * L::B + b * 1024 + lane * 16);
+  };
+  auto afrag = [&](const uint8_t* st, int h, int i) MOE_INLINE {
+    return *reinterpret_cast<const uint4*>(st + h * L::A + aoff + 16 * WM * i * kHalf);
+  };
+#pragma unroll 1
+  for (int cr = 0; cr < n_my; ++cr) {
+    const Item it = cur;
+    const int par = cr & 1;
+    // every wave is done with tile cr - 1: its list makes room for tile cr + 1's
+    lds_barrier();
+    aim(nxt, par ^ 1);
+    cur = nxt;
+    if (cr + 2 < n_my) nxt = item_of(cr + 2);
+    load_list(nxt, par);
+    f32x4 acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int blocks = (it.rows + 15) >> 4;                    // 16-row blocks with rows
+    const int nv = __builtin_amdgcn_readfirstlane(min(MI, max(0, (blocks - wm + WM - 1) / WM)));   // of them this wave's
+    // the K loop over the first NI of the wave's 16-row blocks (one copy for each: a partial tile
+    // skips its empty blocks' products and their scaling)
+    auto run = [&](auto ni) MOE_INLINE {
+      constexpr int NI = decltype(ni)::value;
+#pragma unroll 1
+      for (int kt = 0; kt < nb; ++kt) {
+        wait_loads_barrier<(L::AHEAD - 1) * PER>();            // this stage is complete, every wave is past the last one
+#pragma unroll
+        for (int i = 0; i < PER; ++i) load(i);
+        loaded();
+        const uint8_t* st = next_stage();
+        if constexpr (NI > 0) {
+          // Past K both halves hold the same columns; the rows' second one counts as zeros.  (The weights'
+          // may be NaN, but then so is the first half, which the row multiplies too.)
+          const bool two = 2 * kt + 1 < halves;
+          const float* sc = reinterpret_cast<const float*>(st + 2 * (L::A + L::B));
+          const float* sw = sc + wave * (L::WSCALES / 4) + 32;
+          const float w0 = sw[M == kGateUp || C::BN == kBlock ? 0 : wn], w1 = M == kGateUp ? sw[1] : w0;
+          uint4 a[NI][2];
+          float s[NI][2];
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            a[i][0] = afrag(st, 0, i);
+            a[i][1] = two ? afrag(st, 1, i) : make_uint4(0, 0, 0, 0);
+            const int blk = wm + WM * i;
+            const float sx = sc[(blk % NW) * (L::WSCALES / 4) + (blk / NW) * 16 + l16];
+            s[i][0] = sx * w0;
+            s[i][1] = sx * w1;
+          }
+          if constexpr (EXACT) {
+            Wide x[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x[i] = widen(a[i]);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const uint4 b[2] = {bfrag(st, 0, j), bfrag(st, 1, j)};
+              const Wide w = widen(b);
+#pragma unroll
+              for (int i = 0; i < NI; ++i) {
+                const f32x4 t = mfma_wide(w, x[i]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t[r], s[i][0], acc[i][j][r]);
+              }
+            }
+          } else {
+            // the sums of column block j are scaled into acc while block j + 1 multiplies,
+            // and the operands of block j + 2 are read
+            uint4 b[2] = {bfrag(st, 0, 0), bfrag(st, 1, 0)}, d[2] = {bfrag(st, 0, 1), bfrag(st, 1, 1)};
+            f32x4 t[2][NI];
+#pragma unroll
+            for (int j = 0; j <= NJ; ++j) {
+              uint4 c[2];
+              if (j + 2 < NJ) c[0] = bfrag(st, 0, j + 2), c[1] = bfrag(st, 1, j + 2);
+              if (j < NJ) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) t[j & 1][i] = mfma_codes(b, a[i]);
+              }
+              if (j > 0) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r)
+                    acc[i][j - 1][r] = __builtin_fmaf(t[(j - 1) & 1][i][r], s[i][M == kGateUp && j > NJ / 2 ? 1 : 0], acc[i][j - 1][r]);
+              }
+              if (j > 0 && j < NJ) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // the reads first, then one product, four sums, ...
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                  __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                  __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+                }
+              }
+              __builtin_amdgcn_sched_barrier(0);
+              b[0] = d[0], b[1] = d[1], d[0] = c[0], d[1] = c[1];
+            }
+          }
+        }
+      }
+    };
+    static_assert(MI == 4 || MI == 2, "one copy for each number of blocks");
+    if constexpr (MI == 4) {
+      if (nv == 4) run(std::integral_constant<int, 4>{});
+      else if (nv == 3) run(std::integral_constant<int, 3>{});
+    }
+    if (nv == 2) run(std::integral_constant<int, 2>{});
+    else if (nv == 1) run(std::integral_constant<int, 1>{});
+    else if (nv == 0) run(std::integral_constant<int, 0>{});
+
+    // ---- epilogue
+    const int n0 = it.chunk * OUTC;
+    if constexpr (M == kGateUp) {
+      uint32_t* mx = reinterpret_cast<uint32_t*>(lds + L::MAX);
+      float v[MI][NJ / 2][4];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int blk = wm + WM * i;
+        uint32_t big = 0;
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+          const int c = 16 * (wn * (NJ / 2) + j) + 4 * q;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v[i][j][r] = silu_mul(acc[i][j][r], acc[i][NJ / 2 + j][r]);
+            if (n0 + c < cols) big = max(big, abs_bits(v[i][j][r]));
+          }
+        }
+        big = max_over_q(big);
+        if (q == 0) mx[wn * BM + 16 * blk + l16] = big;
+      }
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = 16 * (wm + WM * i) + l16;
+        if (16 * (wm + WM * i) >= it.rows) continue;           // wave-uniform; the exchange below needs every lane
+        uint32_t big = mx[m];
+#pragma unroll
+        for (int w = 1; w < WN; ++w) big = max(big, mx[w * BM + m]);
+        const Fp8Scale qs = block_scale(big);
+        static_assert(NJ / 2 == 4, "one 16-byte store per row and lane");
+        uint32_t d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = block_codes(v[i][j], qs.r);
+        transpose_rows(d);                                     // now lane 16 q + r: the 16 columns of block q
+        if (m >= it.rows) continue;
+        const int row = it.row(m), n = n0 + 16 * (wn * 4 + q);
+        if (wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.base;
+        if (n < cols)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * cols + n) =
+              make_uint4(d[0], d[1], d[2], d[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int blk = wm + WM * i, m = 16 * blk + l16;
+        if (16 * blk >= it.rows) continue;                     // wave-uniform
+        const bool in = m < it.rows;
+        Out* orow = static_cast<Out*>(p.out) + static_cast<size_t>(it.row(in ? m : 0)) * cols + n0;
+        if constexpr (sizeof(Out) == 4) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const int c = 16 * (wn * NJ + j) + 4 * q;
+            const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            if (in && n0 + c < cols) store4(orow + c, v);
+          }
+        } else {
+          // bf16: two column blocks to 16 bytes a lane: row q = 2 a + b gets columns 8 b .. 8 b + 7 of block j + a
+#pragma unroll
+          for (int j = 0; j < NJ; j += 2) {
+            const f32x4 v = acc[i][j], u = acc[i][j + 1];
+            uint32_t d[4] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
+            swap32(d[0], d[2]);
+            swap32(d[1], d[3]);
+            swap16(d[0], d[2]);
+            swap16(d[1], d[3]);
+            const int c = 16 * (wn * NJ + j + (q >> 1)) + 8 * (q & 1);
+            if (in && n0 + c < cols) *reinterpret_cast<uint4*>(orow + c) = make_uint4(d[0], d[1], d[2], d[3]);
+          }
+        }
+      }
+    }
+  }
+  // the stages requested past the last tile land in LDS: not after this block has left it
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+template <class Tile, Mode M, bool EXACT, class Out>
+void launch_tile(const ProductArgs& p, hipStream_t stream) {
+  const int cus = (device_cus() + kXcds - 1) / kXcds * kXcds;
+  const size_t lds = TileLds<Tile, M>::bytes(p.G);
+  hipLaunchKernelGGL((tile_fp8<Tile, M, EXACT, Out>), dim3(cus), dim3(Tile::NT), lds, stream, p);
+}
+
+Sizes sizes_of(const ProductArgs& p) { return Sizes{p.n_rows, p.E, p.G - p.nseg * p.E, p.nseg, p.K, p.cols}; }
 
 template <Mode M, class Out>
 void launch_product(const ProductArgs& p, hipStream_t stream) {
-  const i8::Sizes s = sizes_of(p);
-  const int nch = (p.cols + kBlock - 1) / kBlock, mf = i8::pick_mf(s.n_rows / s.sequences());
-  const i8::Launch l = i8::launch_of(i8::Plan{i8::Kernel::kStream, mf, item_grid(i8::max_m_tiles(s, 16 * mf), nch)});
-  const dim3 grid(l.x, l.y), block(kThreadsS);
-  if (mf == 1) hipLaunchKernelGGL((stream_fp8<1, M, Out>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((stream_fp8<2, M, Out>), grid, block, 0, stream, p);
+  constexpr bool exact = sizeof(Out) == 4;
+  const Plan plan = fp8::plan(M, exact, sizes_of(p));
+  if (plan.kernel == Kernel::kStream) {
+    const Launch l = launch_of(i8::Plan{i8::Kernel::kStream, plan.width, plan.blocks});
+    const dim3 grid(l.x, l.y), block(kThreadsS);
+    if (plan.width == 1) hipLaunchKernelGGL((stream_fp8<1, M, Out>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((stream_fp8<2, M, Out>), grid, block, 0, stream, p);
+  } else if constexpr (exact) {
+    launch_tile<TileExact, M, true, Out>(p, stream);
+  } else {
+    if (plan.kernel == Kernel::kTileWide) launch_tile<TileWide, M, false, Out>(p, stream);
+    else launch_tile<TileLow, M, false, Out>(p, stream);
+  }
 }
 
 ProductArgs product_args(const GroupedFp8& g, int K, int cols) {

@@ -1,0 +1,78 @@
+// Which kernel runs a block-scaled FP8 product (ffn_fp8.hip) and how much LDS its tiles take, from the
+// sizes alone: host arithmetic without GPU code, so that a host program can ask it too.
+#pragma once
+
+#include "i8_plan.h"
+
+namespace moe {
+namespace fp8 {
+
+using i8::kDown;
+using i8::kGateUp;
+using i8::kLinear;
+using i8::Launch;
+using i8::launch_of;
+using i8::max_m_tiles;
+using i8::Mode;
+using i8::Sizes;
+
+constexpr int kBlock = 128;          // columns that share a scale, and K of a stage
+constexpr int kHalf = 64;            // columns of a packed block
+
+// ---- tile_fp8's tiles and their LDS ---------------------------------------------------
+// MI x NJ blocks of 16x16 per wave, WM x WN waves.
+template <int MI_, int NJ_, int WM_, int WN_>
+struct TileCfg {
+  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = i8::kLanes * NW;
+  static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
+  static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;   // DMA instructions per wave and half
+  static_assert(ADMA >= 1 && ADMA <= 2 && BDMA >= 1, "a wave's rows take lanes 0 - 31 of a load of scales");
+};
+using TileWide = TileCfg<4, 8, 4, 2>;    // 256 rows x 256 weight rows
+using TileLow = TileCfg<2, 8, 4, 2>;     // 128 rows x 256
+using TileExact = TileCfg<4, 4, 4, 2>;   // 256 rows x 128
+
+constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile (TileLds)
+template <class C, Mode M>
+struct TileLds {
+  static constexpr int A = C::BM * kHalf, B = C::BN * kHalf;   // bytes of half a stage
+  static constexpr int WSCALES = 144;                          // a wave's: 32 rows, two blocks of the matrix
+  static constexpr int STAGE = 2 * (A + B) + C::NW * WSCALES;
+  static constexpr int WROWS = 16 * C::ADMA * 4, ROWS = C::NW * WROWS;
+  static constexpr int FIXED = 2 * ROWS + (M == kGateUp ? C::WN * C::BM * 4 : 0);
+  static constexpr int plan_bytes(int G) { return 4 * C::NW + 8 * (G + 1); }
+  static constexpr int kMostGroups = 2 * 512 + 256;
+  static constexpr int STAGES = (i8::kLdsPerCu - FIXED - plan_bytes(kMostGroups)) / STAGE;
+  static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
+  static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int LIST = RING;                            // row list of two tiles
+  static constexpr int MAX = LIST + 2 * ROWS;                  // kGateUp: largest magnitudes
+  static constexpr int PLAN = RING + FIXED;                    // sums over waves, tiles before each group, group offsets
+  static int bytes(int G) { return PLAN + plan_bytes(G); }
+  // The stages requested before a block's first product stop short of its first tile's last one: what
+  // follows it is the next tile's, whose sources are set when the first tile starts.
+  static_assert(AHEAD < kTileMinStages, "a tile has more stages than are requested ahead");
+};
+
+enum class Kernel { kStream, kTileLow, kTileWide, kTileExact };
+struct Plan {
+  Kernel kernel;
+  int width;    // stream_fp8: 16-row blocks of a tile
+  int blocks;   // stream_fp8: blocks of the launch (tile_fp8's walk a list)
+};
+
+constexpr int kTileMinAvg = 64, kWideMinAvg = 192;
+constexpr int kTileMinItems = 512;
+
+inline Plan plan(Mode m, bool exact, const Sizes& s) {
+  const int avg = s.n_rows / s.sequences();
+  const long long area = static_cast<long long>(s.n_rows) * s.cols;
+  if (avg > kTileMinAvg && area >= kTileMinItems * 64ll * 128 && s.K > (kTileMinStages - 1) * kBlock)
+    return Plan{exact ? Kernel::kTileExact : avg >= kWideMinAvg ? Kernel::kTileWide : Kernel::kTileLow, 0, 0};
+  const int nch = (s.cols + kBlock - 1) / kBlock, mf = i8::pick_mf(avg);
+  return Plan{Kernel::kStream, mf, item_grid(max_m_tiles(s, 16 * mf), nch)};
+}
+
+}  // namespace fp8
+}  // namespace moe
