@@ -291,6 +291,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   const int nb = (K + kBlock - 1) / kBlock, ncb = (cols + kBlock - 1) / kBlock;
 
   for (int g = tid; g <= p.G; g += NT) offs[g] = p.offs[g];
+  if (tid < 4) reinterpret_cast<uint32_t*>(lds + L::ZERO)[tid] = 0;
   __syncthreads();
   {
     int cnt[GPT], sum = 0;
@@ -343,13 +344,14 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   // ---- the loads, STAGES - 1 stages ahead of the products
   const uint32_t lds0 = lds_address(lds);
   const int halves = K / kHalf;
-  uint32_t ao[C::ADMA], ao_next[C::ADMA];                      // this lane's bytes from p.a: tile being loaded, tile after it
-  const uint8_t *bp[C::BDMA], *bp_next[C::BDMA];               // wave-uniform
-  const float *sp, *sp_next;                                   // this lane's scales, one per stage, sstep apart
+  uint32_t ao[C::ADMA];                                        // of the tile being loaded: this lane's bytes from p.a,
+  const uint8_t* bp[C::BDMA];                                  // the weights (wave-uniform),
+  const float* sp;                                             // this lane's scales, one per stage, sstep apart
   // lane 16 i + r of a wave has row r of the 16 rows of its load i, so wave w's rows are the w-th 16 * ADMA of ROWS
-  const bool vlane = lane < 16 * C::ADMA, slane = vlane || (lane >> 1) == 16;
+  const bool vlane = lane < 16 * C::ADMA;
+  constexpr uint64_t kScaleLanes = ((1ull << 16 * C::ADMA) - 1) | 3ull << 32;
   const int vrow = 16 * (wave + NW * (lane >> 4)) + l16;
-  const size_t sstep = lane < 32 ? p.as_block : 1;
+  const uint32_t sstep = lane < 32 ? static_cast<uint32_t>(p.as_block) : 1;   // blocks times as_block: below 2^31
   auto load_list = [&](const Item& it, int parity) MOE_INLINE {
     if (p.x_rows && vlane)
       dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * L::WROWS);
@@ -363,7 +365,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
 #pragma unroll
     for (int i = 0; i < C::ADMA; ++i) {
       const int r = 16 * (wave + NW * i) + (lane >> 2);
-      ao_next[i] = static_cast<uint32_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
+      ao[i] = static_cast<uint32_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
     }
     const int n0 = it.chunk * OUTC;
     const size_t e0 = static_cast<size_t>(it.expert) * cols;
@@ -372,28 +374,20 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
       const int b = wave + NW * i;                             // 16-row block of the tile
       const bool up = M == kGateUp && b >= C::BN / 32;
       const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
-      bp_next[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
+      bp[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
     }
     const int second = lane & 1;
     const int cb = M == kGateUp ? it.chunk : min(it.chunk * (OUTC / kBlock) + second, ncb - 1);
     const float* sw = (M == kGateUp && second ? p.s1 : p.s0) + (static_cast<size_t>(it.expert) * ncb + cb) * nb;
-    sp_next = vlane ? p.as + src(vrow, lane & (16 * C::ADMA - 1)) * p.as_row : sw;
+    sp = vlane ? p.as + src(vrow, lane & (16 * C::ADMA - 1)) * p.as_row : sw;
   };
   int ikt = 0, islot = 0;                                      // the stage requested next: of its tile, ring slot
-  auto turn = [&]() MOE_INLINE {                               // go on with the next tile
-    ikt = 0;
-#pragma unroll
-    for (int i = 0; i < C::ADMA; ++i) ao[i] = ao_next[i];
-#pragma unroll
-    for (int i = 0; i < C::BDMA; ++i) bp[i] = bp_next[i];
-    sp = sp_next;
-  };
   constexpr int CODES = 2 * (C::ADMA + C::BDMA);               // loads of a stage per wave: of codes,
   constexpr int PER = CODES + 1;                               // and one of scales
   auto load = [&](int i) MOE_INLINE {                          // the i-th of them
     const uint32_t st = lds0 + islot * L::STAGE;
     if (i == CODES) {
-      if (slane) dma4(sp + ikt * sstep, st + 2 * (L::A + L::B) + wave * L::WSCALES);
+      dma4(sp + ikt * sstep, st + 2 * (L::A + L::B) + wave * L::WSCALES, kScaleLanes);
       return;
     }
     const int h = i / (C::ADMA + C::BDMA), n = i % (C::ADMA + C::BDMA);
@@ -404,140 +398,153 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   };
   auto loaded = [&]() MOE_INLINE {
     islot = islot + 1 == L::STAGES ? 0 : islot + 1;
-    if (++ikt == nb) turn();
+    ++ikt;
   };
   Item cur = item_of(0), nxt = n_my > 1 ? item_of(1) : cur;
   load_list(cur, 0);
   load_list(nxt, 1);
   wait_loads_barrier<0>();
   aim(cur, 0);
-  turn();
+  constexpr int EARLY = PER * 2 / (NJ - 1);                    // loads of a stage that are requested in its step's last two passes
 #pragma unroll 1
-  for (int s = 0; s < L::AHEAD; ++s) {                         // nb > AHEAD (kTileMinStages)
+  for (int s = 0; s < L::AHEAD - 1; ++s) {                     // nb >= AHEAD (kTileMinStages)
 #pragma unroll
     for (int i = 0; i < PER; ++i) load(i);
     loaded();
   }
+#pragma unroll
+  for (int i = 0; i < EARLY; ++i) load(i);
 
   // ---- compute side
+  // A step multiplies a stage: a pass for each of the wave's column blocks over its row blocks.  Nothing waits
+  // for LDS: a column block is read two passes ahead, the next stage's rows in the last pass, each into the registers
+  // of the ones that it has just used; and the loads of the stages to come are spread over the passes.
   const int aoff = 16 * wm * kHalf + l16 * kHalf + 16 * (q ^ swz(l16));   // 16-row blocks do not change swz
-  int cslot = 0;
-  auto next_stage = [&]() MOE_INLINE {
-    const uint8_t* st = lds + cslot * L::STAGE;
-    cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
-    return st;
+  uint4 fa[MI][2], fb[4][2];
+  float sx[MI], sw[2];
+  uint32_t cslot = 0, st = 0;                                  // the stage that is read: ring slot, place in LDS
+  int ckt = 0;                                                 // its number in its tile
+  auto at16 = [&](uint32_t a) MOE_INLINE { return *reinterpret_cast<const uint4*>(lds + a); };
+  auto at4 = [&](uint32_t a) MOE_INLINE { return *reinterpret_cast<const float*>(lds + a); };
+  auto read_a = [&](int i) MOE_INLINE {
+    // Past K both halves hold the same columns; the rows' second one is read from zeros.  (The weights'
+    // may be NaN, but then so is the first half, which the row multiplies too.)
+    const uint32_t a = st + aoff + 16 * WM * i * kHalf;
+    fa[i][0] = at16(a);
+    fa[i][1] = at16(2 * ckt + 1 < halves ? a + L::A : L::ZERO);
   };
-  auto bfrag = [&](const uint8_t* st, int h, int j) MOE_INLINE {
+  auto read_b = [&](int j) MOE_INLINE {
     const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2) : wn * NJ + j;
-    return *reinterpret_cast<const uint4*>(st + 2 * L::A + h * L::B + b * 1024 + lane * 16);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fb[j & 3][h] = at16(st + 2 * L::A + h * L::B + b * 1024 + lane * 16);
   };
-  auto afrag = [&](const uint8_t* st, int h, int i) MOE_INLINE {
-    return *reinterpret_cast<const uint4*>(st + h * L::A + aoff + 16 * WM * i * kHalf);
+  auto read_scales = [&]() MOE_INLINE {
+    const uint32_t sc = st + 2 * (L::A + L::B);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int blk = wm + WM * i;
+      sx[i] = at4(sc + (blk % NW) * L::WSCALES + (blk / NW) * 64 + l16 * 4);
+    }
+    const uint32_t w = sc + wave * L::WSCALES + 128;
+    sw[0] = at4(w + 4 * (M == kGateUp || C::BN == kBlock ? 0 : wn * NJ * 16 / kBlock));
+    sw[1] = M == kGateUp ? at4(w + 4) : sw[0];
   };
+  wait_loads_barrier<(L::AHEAD - 2) * PER + EARLY>();
+  read_scales();
+#pragma unroll
+  for (int i = 0; i < MI; ++i) read_a(i);
+  read_b(0);
+  read_b(1);
 #pragma unroll 1
   for (int cr = 0; cr < n_my; ++cr) {
     const Item it = cur;
     const int par = cr & 1;
-    // every wave is done with tile cr - 1: its list makes room for tile cr + 1's
-    lds_barrier();
-    aim(nxt, par ^ 1);
     cur = nxt;
     if (cr + 2 < n_my) nxt = item_of(cr + 2);
-    load_list(nxt, par);
+    load_list(nxt, par);                                       // in place of tile cr's
     f32x4 acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int blocks = (it.rows + 15) >> 4;                    // 16-row blocks with rows
-    const int nv = __builtin_amdgcn_readfirstlane(min(MI, max(0, (blocks - wm + WM - 1) / WM)));   // of them this wave's
-    // the K loop over the first NI of the wave's 16-row blocks (one copy for each: a partial tile
-    // skips its empty blocks' products and their scaling)
-    auto run = [&](auto ni) MOE_INLINE {
-      constexpr int NI = decltype(ni)::value;
-#pragma unroll 1
-      for (int kt = 0; kt < nb; ++kt) {
-        wait_loads_barrier<(L::AHEAD - 1) * PER>();            // this stage is complete, every wave is past the last one
+    // A product is scaled into acc LAG products later; the step's last ones in the next step.
+    constexpr int LAG = EXACT ? MI : 3, RING = EXACT ? 2 * MI : 4, ALL = MI * NJ;
+    f32x4 t[RING];
+    float s[2][MI], s_last[MI];                                // rows' times gate's (the only), up's; of the step before
 #pragma unroll
-        for (int i = 0; i < PER; ++i) load(i);
-        loaded();
-        const uint8_t* st = next_stage();
-        if constexpr (NI > 0) {
-          // Past K both halves hold the same columns; the rows' second one counts as zeros.  (The weights'
-          // may be NaN, but then so is the first half, which the row multiplies too.)
-          const bool two = 2 * kt + 1 < halves;
-          const float* sc = reinterpret_cast<const float*>(st + 2 * (L::A + L::B));
-          const float* sw = sc + wave * (L::WSCALES / 4) + 32;
-          const float w0 = sw[M == kGateUp || C::BN == kBlock ? 0 : wn], w1 = M == kGateUp ? sw[1] : w0;
-          uint4 a[NI][2];
-          float s[NI][2];
+    for (int i = 0; i < RING; ++i) t[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            a[i][0] = afrag(st, 0, i);
-            a[i][1] = two ? afrag(st, 1, i) : make_uint4(0, 0, 0, 0);
-            const int blk = wm + WM * i;
-            const float sx = sc[(blk % NW) * (L::WSCALES / 4) + (blk / NW) * 16 + l16];
-            s[i][0] = sx * w0;
-            s[i][1] = sx * w1;
-          }
-          if constexpr (EXACT) {
-            Wide x[NI];
+    for (int i = 0; i < MI; ++i) s_last[i] = 0.f;
+    auto add = [&](int n) MOE_INLINE {                         // product n of this step, n < 0: of the step before
+      const int m = (n + ALL) % ALL, i = m % MI, j = m / MI;
+      const float by = n < 0 ? s_last[i] : s[M == kGateUp && j >= NJ / 2 ? 1 : 0][i];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) x[i] = widen(a[i]);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const uint4 b[2] = {bfrag(st, 0, j), bfrag(st, 1, j)};
-              const Wide w = widen(b);
-#pragma unroll
-              for (int i = 0; i < NI; ++i) {
-                const f32x4 t = mfma_wide(w, x[i]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t[r], s[i][0], acc[i][j][r]);
-              }
-            }
-          } else {
-            // the sums of column block j are scaled into acc while block j + 1 multiplies,
-            // and the operands of block j + 2 are read
-            uint4 b[2] = {bfrag(st, 0, 0), bfrag(st, 1, 0)}, d[2] = {bfrag(st, 0, 1), bfrag(st, 1, 1)};
-            f32x4 t[2][NI];
-#pragma unroll
-            for (int j = 0; j <= NJ; ++j) {
-              uint4 c[2];
-              if (j + 2 < NJ) c[0] = bfrag(st, 0, j + 2), c[1] = bfrag(st, 1, j + 2);
-              if (j < NJ) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) t[j & 1][i] = mfma_codes(b, a[i]);
-              }
-              if (j > 0) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r)
-                    acc[i][j - 1][r] = __builtin_fmaf(t[(j - 1) & 1][i][r], s[i][M == kGateUp && j > NJ / 2 ? 1 : 0], acc[i][j - 1][r]);
-              }
-              if (j > 0 && j < NJ) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // the reads first, then one product, four sums, ...
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                  __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                  __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
-                }
-              }
-              __builtin_amdgcn_sched_barrier(0);
-              b[0] = d[0], b[1] = d[1], d[0] = c[0], d[1] = c[1];
-            }
-          }
-        }
-      }
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t[m % RING][r], by, acc[i][j][r]);
     };
-    static_assert(MI == 4 || MI == 2, "one copy for each number of blocks");
-    if constexpr (MI == 4) {
-      if (nv == 4) run(std::integral_constant<int, 4>{});
-      else if (nv == 3) run(std::integral_constant<int, 3>{});
+#pragma unroll 1
+    for (int kt = 0; kt < nb; ++kt) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        s[0][i] = sx[i] * sw[0];
+        s[1][i] = sx[i] * sw[1];
+      }
+      Wide x[EXACT ? MI : 1];
+      if constexpr (EXACT) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) x[i] = widen(fa[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (j == NJ - 2) {
+          // the next stage is complete in LDS, and every wave has read all of this one
+          wait_loads_reads_barrier<(L::AHEAD - 2) * PER>();
+          cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
+          ckt = ckt + 1 == nb ? 0 : ckt + 1;
+          st = cslot * L::STAGE;
+          // (sums up to here are made here: the compiler would move them behind the branch, and keep all products)
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int m = 0; m < NJ; ++m) asm volatile("" : "+v"(acc[i][m]));
+          if (ikt == nb) {                                     // go on with the next tile's stages
+            aim(cur, par ^ 1);
+            ikt = 0;
+          }
+          read_scales();
+        }
+        read_b((j + 2) % NJ);
+        if constexpr (EXACT) {
+          const Wide w = widen(fb[j & 3]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              f32x4& to = t[(j * MI + i) % RING];
+              to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x[EXACT ? i : 0].v[h], h ? to : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          if constexpr (!EXACT) t[(j * MI + i) % RING] = mfma_codes(fb[j & 3], fa[i]);
+          if (j == NJ - 1) read_a(i);
+          add(j * MI + i - LAG);
+        }
+        // a stage's loads: the first EARLY in the last two passes, the others in all but the last three
+        if (j >= NJ - 2) {
+#pragma unroll
+          for (int l = (j - (NJ - 2)) * EARLY / 2; l < (j - (NJ - 3)) * EARLY / 2; ++l) load(l);
+        } else if (j < NJ - 3) {
+#pragma unroll
+          for (int l = EARLY + j * (PER - EARLY) / (NJ - 3); l < EARLY + (j + 1) * (PER - EARLY) / (NJ - 3); ++l) load(l);
+          if (j == NJ - 4) loaded();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) s_last[i] = s[M == kGateUp ? 1 : 0][i];
     }
-    if (nv == 2) run(std::integral_constant<int, 2>{});
-    else if (nv == 1) run(std::integral_constant<int, 1>{});
-    else if (nv == 0) run(std::integral_constant<int, 0>{});
+#pragma unroll
+    for (int n = -LAG; n < 0; ++n) add(n);
 
     // ---- epilogue
     const int n0 = it.chunk * OUTC;
@@ -569,17 +576,23 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
 #pragma unroll
         for (int w = 1; w < WN; ++w) big = max(big, mx[w * BM + m]);
         const Fp8Scale qs = block_scale(big);
-        static_assert(NJ / 2 == 4, "one 16-byte store per row and lane");
-        uint32_t d[4];
+        uint32_t d[NJ / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = block_codes(v[i][j], qs.r);
-        transpose_rows(d);                                     // now lane 16 q + r: the 16 columns of block q
-        if (m >= it.rows) continue;
-        const int row = it.row(m), n = n0 + 16 * (wn * 4 + q);
-        if (wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.base;
-        if (n < cols)
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * cols + n) =
-              make_uint4(d[0], d[1], d[2], d[3]);
+        for (int j = 0; j < NJ / 2; ++j) d[j] = block_codes(v[i][j], qs.r);
+        const int row = it.row(min(m, it.rows - 1));
+        uint8_t* orow = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * cols;
+        if (m < it.rows && wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.base;
+        if constexpr (NJ / 2 == 4) {
+          transpose_rows(d);                                   // now lane 16 q + r: the 16 columns of block q
+          const int n = n0 + 16 * (wn * 4 + q);
+          if (m < it.rows && n < cols) *reinterpret_cast<uint4*>(orow + n) = make_uint4(d[0], d[1], d[2], d[3]);
+        } else {
+          static_assert(NJ / 2 == 2, "one store per row and lane");
+          swap32(d[0], d[1]);                                  // row q = 2 a + b gets columns 8 b .. 8 b + 7 of block a
+          swap16(d[0], d[1]);
+          const int n = n0 + 16 * (wn * 2 + (q >> 1)) + 8 * (q & 1);
+          if (m < it.rows && n < cols) *reinterpret_cast<uint2*>(orow + n) = make_uint2(d[0], d[1]);
+        }
       }
     } else {
 #pragma unroll

@@ -29,7 +29,7 @@ struct TileCfg {
   static_assert(ADMA >= 1 && ADMA <= 2 && BDMA >= 1, "a wave's rows take lanes 0 - 31 of a load of scales");
 };
 using TileWide = TileCfg<4, 8, 4, 2>;    // 256 rows x 256 weight rows
-using TileLow = TileCfg<2, 8, 4, 2>;     // 128 rows x 256
+using TileLow = TileCfg<4, 4, 2, 4>;     // 128 rows x 256
 using TileExact = TileCfg<4, 4, 4, 2>;   // 256 rows x 128
 
 constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile (TileLds)
@@ -39,20 +39,21 @@ struct TileLds {
   static constexpr int WSCALES = 144;                          // a wave's: 32 rows, two blocks of the matrix
   static constexpr int STAGE = 2 * (A + B) + C::NW * WSCALES;
   static constexpr int WROWS = 16 * C::ADMA * 4, ROWS = C::NW * WROWS;
-  static constexpr int FIXED = 2 * ROWS + (M == kGateUp ? C::WN * C::BM * 4 : 0);
+  static constexpr int FIXED = 2 * ROWS + (M == kGateUp ? C::WN * C::BM * 4 : 0) + 16;
   static constexpr int plan_bytes(int G) { return 4 * C::NW + 8 * (G + 1); }
   static constexpr int kMostGroups = 2 * 512 + 256;
   static constexpr int STAGES = (i8::kLdsPerCu - FIXED - plan_bytes(kMostGroups)) / STAGE;
-  static constexpr int AHEAD = STAGES - 1;                     // stages requested before the first is used
+  static constexpr int AHEAD = STAGES;                         // stages requested before the first is multiplied
   static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
-  static constexpr int RING = STAGES * STAGE;
+  static constexpr int RING = STAGES * STAGE, PLAN_ = RING + FIXED;
   static constexpr int LIST = RING;                            // row list of two tiles
   static constexpr int MAX = LIST + 2 * ROWS;                  // kGateUp: largest magnitudes
-  static constexpr int PLAN = RING + FIXED;                    // sums over waves, tiles before each group, group offsets
+  static constexpr int ZERO = PLAN_ - 16;                      // zeros
+  static constexpr int PLAN = PLAN_;                    // sums over waves, tiles before each group, group offsets
   static int bytes(int G) { return PLAN + plan_bytes(G); }
-  // The stages requested before a block's first product stop short of its first tile's last one: what
-  // follows it is the next tile's, whose sources are set when the first tile starts.
-  static_assert(AHEAD < kTileMinStages, "a tile has more stages than are requested ahead");
+  // The stages requested before a block's first product are all its first tile's: what follows is
+  // the next tile's, whose sources are set when the first tile starts.
+  static_assert(AHEAD <= kTileMinStages, "a tile has more stages than are requested ahead");
 };
 
 enum class Kernel { kStream, kTileLow, kTileWide, kTileExact };

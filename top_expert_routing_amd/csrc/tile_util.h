@@ -120,9 +120,20 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
   asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
+// The same for the lanes of `mask`, without a branch (which would end the block of instructions that the
+// compiler schedules).  Every lane of the wave takes part.
+__device__ __forceinline__ void dma4(const void* g, uint32_t lds, uint64_t mask) {
+  asm volatile("s_nop 4\n\ts_mov_b64 exec, %1\n\tglobal_load_lds_dword %0, off\n\ts_mov_b64 exec, -1"
+               : : "v"(g), "s"(mask), "{m0}"(lds) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_loads_barrier() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+// The same, and the wave's LDS reads are done: what all waves have read may be overwritten.
+template <int N>
+__device__ __forceinline__ void wait_loads_reads_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 // LDS writes of all waves before LDS reads of all waves, DMA loads left in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
