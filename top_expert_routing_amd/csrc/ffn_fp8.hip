@@ -262,17 +262,23 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_fp8(ProductArgs p) {
 // (kGateUp: 128 gate and the same 128 up rows).  K advances 128 codes a stage through a
 // ring of LDS stages that LDS-DMA loads fill ahead; the stages of all tiles form one
 // stream, so the next tile's first stages load while this one finishes.
-//   * rows: a stage holds them as two halves of 64 codes, four 16-byte pieces each; piece c of row
-//     r lies at slot c ^ swz(r), so that the 16 rows of an operand read hit different banks.  A DMA
-//     instruction fills 16 rows (lane -> row lane / 4, slot lane % 4).
+//   * rows: 128 bytes of a row per stage, eight 16-byte pieces; piece c of row r lies at slot
+//     c ^ ((r / 2) % 8), so that the 16 rows of an operand read hit different banks.  A DMA instruction
+//     fills 8 rows (lane -> row lane / 8, slot lane % 8): whole cache lines, whose number bounds the loads.
 //   * weights: a packed block (16 rows x 64 codes, 1 KiB) is copied as it is.
-//   * scales: one 4-byte load per wave and stage, its rows' in lanes 0 - 31, the matrix's (kGateUp:
-//     gate's and up's, else those of the tile's two blocks of 128 columns) in lanes 32 and 33.
+//   * scales: those of four stages together, since a row's lie in one cache line: a 4-byte load for
+//     each 16 of a wave's rows (lane 4 r + k: row r, stage k), and one for the matrix's (kGateUp: gate's and
+//     up's, else those of the tile's two blocks of 128 columns), one load per stage.
 //   * the row list comes by DMA too, a tile ahead, because a load that the compiler sees would
 //     make it wait for everything in flight.
 // Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave, so the
 // rows of a partial tile spread over them.
-__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+// The lane's number, made anew: what is computed from it outside the K loop does not stay in registers through it.
+__device__ __forceinline__ int fresh_lane() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+  return l;
+}
 
 template <class C, Mode M, bool EXACT, class Out>
 __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
@@ -344,29 +350,34 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   // ---- the loads, STAGES - 1 stages ahead of the products
   const uint32_t lds0 = lds_address(lds);
   const int halves = K / kHalf;
-  uint32_t ao[C::ADMA];                                        // of the tile being loaded: this lane's bytes from p.a,
+  uint32_t ao[2 * C::ADMA];                                    // of the tile being loaded: this lane's bytes from p.a,
+  uint32_t so[C::ADMA];                                        // its rows' scales, in floats from p.as,
   const uint8_t* bp[C::BDMA];                                  // the weights (wave-uniform),
-  const float* sp;                                             // this lane's scales, one per stage, sstep apart
-  // lane 16 i + r of a wave has row r of the 16 rows of its load i, so wave w's rows are the w-th 16 * ADMA of ROWS
-  const bool vlane = lane < 16 * C::ADMA;
-  constexpr uint64_t kScaleLanes = ((1ull << 16 * C::ADMA) - 1) | 3ull << 32;
-  const int vrow = 16 * (wave + NW * (lane >> 4)) + l16;
-  const uint32_t sstep = lane < 32 ? static_cast<uint32_t>(p.as_block) : 1;   // blocks times as_block: below 2^31
+  const float *wp0, *wp1;                                      // the matrix's scales (wave-uniform),
+  const uint32_t last = static_cast<uint32_t>(p.n_x) * K - 16; // no row piece starts later: a short last stage's pieces past K
+                                                               // are another row's, and not used (read_a)
+  // lane 16 i + r of a wave has row r of the 16 rows of its block i, so wave w's rows are the w-th 16 * ADMA of ROWS
+  const uint32_t as_row = static_cast<uint32_t>(p.as_row), as_block = static_cast<uint32_t>(p.as_block);
   auto load_list = [&](const Item& it, int parity) MOE_INLINE {
-    if (p.x_rows && vlane)
-      dma4(p.x_rows + it.row(min(vrow, it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * L::WROWS);
+    const int lane = fresh_lane();
+    if (p.x_rows && lane < 16 * C::ADMA)
+      dma4(p.x_rows + it.row(min(16 * (wave + NW * (lane >> 4)) + (lane & 15), it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * L::WROWS);
   };
   // Sources of a tile whose row list has arrived.
   auto aim = [&](const Item& it, int parity) MOE_INLINE {
+    const int lane = fresh_lane();
     const int* list = reinterpret_cast<const int*>(lds + L::LIST + parity * L::ROWS + wave * L::WROWS);
     auto src = [&](int r, int slot) MOE_INLINE {
       return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : it.row(min(r, it.rows - 1));
     };
 #pragma unroll
-    for (int i = 0; i < C::ADMA; ++i) {
-      const int r = 16 * (wave + NW * i) + (lane >> 2);
-      ao[i] = static_cast<uint32_t>(src(r, 16 * i + (lane >> 2))) * K + 16 * ((lane & 3) ^ swz(r));
+    for (int i = 0; i < 2 * C::ADMA; ++i) {
+      const int t = 8 * (i & 1) + (lane >> 3);                 // row of the 16
+      ao[i] = static_cast<uint32_t>(src(16 * (wave + NW * (i >> 1)) + t, 16 * (i >> 1) + t)) * K + 16 * ((lane & 7) ^ ((t >> 1) & 7));
     }
+#pragma unroll
+    for (int i = 0; i < C::ADMA; ++i)
+      so[i] = src(16 * (wave + NW * i) + (lane >> 2), 16 * i + (lane >> 2)) * as_row + (lane & 3) * as_block;
     const int n0 = it.chunk * OUTC;
     const size_t e0 = static_cast<size_t>(it.expert) * cols;
 #pragma unroll
@@ -376,25 +387,38 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
       const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
       bp[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
     }
-    const int second = lane & 1;
-    const int cb = M == kGateUp ? it.chunk : min(it.chunk * (OUTC / kBlock) + second, ncb - 1);
-    const float* sw = (M == kGateUp && second ? p.s1 : p.s0) + (static_cast<size_t>(it.expert) * ncb + cb) * nb;
-    sp = vlane ? p.as + src(vrow, lane & (16 * C::ADMA - 1)) * p.as_row : sw;
+    const size_t sb = static_cast<size_t>(it.expert) * ncb;
+    wp0 = p.s0 + (sb + (M == kGateUp ? it.chunk : it.chunk * (OUTC / kBlock))) * nb;
+    wp1 = M == kGateUp ? p.s1 + (sb + it.chunk) * nb : p.s0 + (sb + min(it.chunk * (OUTC / kBlock) + 1, ncb - 1)) * nb;
   };
   int ikt = 0, islot = 0;                                      // the stage requested next: of its tile, ring slot
-  constexpr int CODES = 2 * (C::ADMA + C::BDMA);               // loads of a stage per wave: of codes,
-  constexpr int PER = CODES + 1;                               // and one of scales
-  auto load = [&](int i) MOE_INLINE {                          // the i-th of them
-    const uint32_t st = lds0 + islot * L::STAGE;
-    if (i == CODES) {
-      dma4(sp + ikt * sstep, st + 2 * (L::A + L::B) + wave * L::WSCALES, kScaleLanes);
-      return;
+  int gload = 0;                                               // slot of the group of scales requested last
+  // Part u of a group's scales: 16 of the rows', the matrix's; lanes past K's blocks take no part.
+  auto load_scales = [&](int group, int slot, int u) MOE_INLINE {
+    const int left = nb - group * kScaleGroup;
+    const uint64_t four = left >= kScaleGroup ? 15 : left > 0 ? (1 << left) - 1 : 0;
+    const uint32_t to = lds0 + L::SCALE0 + slot * L::SCALES + wave * L::WSCALES;
+    if (u < C::ADMA) {
+      uint32_t o = so[0];
+#pragma unroll
+      for (int i = 1; i < C::ADMA; ++i) o = u == i ? so[i] : o;
+      dma4(p.as, (o + group * kScaleGroup * as_block) * 4, to + u * 256, four * 0x1111111111111111ull);
+    } else if (u == C::ADMA) {
+      const int lane = fresh_lane();
+      dma4((lane & 4 ? wp1 : wp0) + group * kScaleGroup + (lane & 3), to + u * 256, four * 0x11ull);
     }
-    const int h = i / (C::ADMA + C::BDMA), n = i % (C::ADMA + C::BDMA);
-    const int kt = min(2 * ikt + h, halves - 1);               // the half past K: the last one again (see a1 below)
-    if (n < C::ADMA) dma16(p.a + kt * kHalf, ao[n], st + h * L::A + (n * NW + wave) * 1024);
-    else dma16(bp[n - C::ADMA] + static_cast<size_t>(kt) * 1024, lane * 16,
-               st + 2 * L::A + h * L::B + ((n - C::ADMA) * NW + wave) * 1024);
+  };
+  constexpr int PER = 2 * (C::ADMA + C::BDMA);                 // loads of a stage's codes per wave
+  auto load = [&](int i) MOE_INLINE {                          // the i-th of them
+    const uint32_t to = lds0 + islot * L::STAGE;
+    if (i < 2 * C::ADMA) {
+      const uint32_t k = ikt * kBlock;
+      dma16(p.a + k, min(ao[i], last - k), to + ((i >> 1) * NW + wave) * 2048 + (i & 1) * 1024);
+    } else {
+      const int h = (i - 2 * C::ADMA) / C::BDMA, n = (i - 2 * C::ADMA) % C::BDMA;
+      const int kt = min(2 * ikt + h, halves - 1);             // the half past K: the last one again (read_a)
+      dma16(bp[n] + static_cast<size_t>(kt) * 1024, lane * 16, to + L::A + h * L::B + (n * NW + wave) * 1024);
+    }
   };
   auto loaded = [&]() MOE_INLINE {
     islot = islot + 1 == L::STAGES ? 0 : islot + 1;
@@ -405,13 +429,25 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   load_list(nxt, 1);
   wait_loads_barrier<0>();
   aim(cur, 0);
+#pragma unroll
+  for (int u = 0; u <= C::ADMA; ++u) load_scales(0, 0, u);
+  // Where a stage's loads begin: its part of the scales of the group after its own.  Three slots are enough with
+  // two stages ahead: the group that a slot held was read to its end when a stage of the third one begins.
+  static_assert(L::AHEAD == 2, "three groups of scales");
+  auto begin_stage = [&]() MOE_INLINE {
+    const int u = ikt % kScaleGroup;
+    if (u == 0) gload = gload + 1 == L::GROUPS ? 0 : gload + 1;
+    load_scales(ikt / kScaleGroup + 1, gload, u);
+  };
   constexpr int EARLY = PER * 2 / (NJ - 1);                    // loads of a stage that are requested in its step's last two passes
 #pragma unroll 1
   for (int s = 0; s < L::AHEAD - 1; ++s) {                     // nb >= AHEAD (kTileMinStages)
+    begin_stage();
 #pragma unroll
     for (int i = 0; i < PER; ++i) load(i);
     loaded();
   }
+  begin_stage();
 #pragma unroll
   for (int i = 0; i < EARLY; ++i) load(i);
 
@@ -419,9 +455,10 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   // A step multiplies a stage: a pass for each of the wave's column blocks over its row blocks.  Nothing waits
   // for LDS: a column block is read two passes ahead, the next stage's rows in the last pass, each into the registers
   // of the ones that it has just used; and the loads of the stages to come are spread over the passes.
-  const int aoff = 16 * wm * kHalf + l16 * kHalf + 16 * (q ^ swz(l16));   // 16-row blocks do not change swz
+  const uint32_t aoff = (16 * wm + l16) * kBlock + 16 * (q ^ (l16 >> 1));   // piece q; piece q + 4 is 64 bytes up or down
   uint4 fa[MI][2], fb[4][2];
   float sx[MI], sw[2];
+  int cgroup = 0;                                              // slot of the scales that are read
   uint32_t cslot = 0, st = 0;                                  // the stage that is read: ring slot, place in LDS
   int ckt = 0;                                                 // its number in its tile
   auto at16 = [&](uint32_t a) MOE_INLINE { return *reinterpret_cast<const uint4*>(lds + a); };
@@ -429,25 +466,25 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   auto read_a = [&](int i) MOE_INLINE {
     // Past K both halves hold the same columns; the rows' second one is read from zeros.  (The weights'
     // may be NaN, but then so is the first half, which the row multiplies too.)
-    const uint32_t a = st + aoff + 16 * WM * i * kHalf;
-    fa[i][0] = at16(a);
-    fa[i][1] = at16(2 * ckt + 1 < halves ? a + L::A : L::ZERO);
+    const uint32_t a = st + aoff;
+    fa[i][0] = at16(a + 16 * WM * i * kBlock);
+    fa[i][1] = at16(2 * ckt + 1 < halves ? (a ^ 64) + 16 * WM * i * kBlock : L::ZERO);
   };
   auto read_b = [&](int j) MOE_INLINE {
     const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2) : wn * NJ + j;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) fb[j & 3][h] = at16(st + 2 * L::A + h * L::B + b * 1024 + lane * 16);
+    for (int h = 0; h < 2; ++h) fb[j & 3][h] = at16(st + L::A + h * L::B + b * 1024 + lane * 16);
   };
   auto read_scales = [&]() MOE_INLINE {
-    const uint32_t sc = st + 2 * (L::A + L::B);
+    const uint32_t sc = L::SCALE0 + cgroup * L::SCALES + ckt % kScaleGroup * 4;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const int blk = wm + WM * i;
-      sx[i] = at4(sc + (blk % NW) * L::WSCALES + (blk / NW) * 64 + l16 * 4);
+      sx[i] = at4(sc + (blk % NW) * L::WSCALES + (blk / NW) * 256 + l16 * 16);
     }
-    const uint32_t w = sc + wave * L::WSCALES + 128;
-    sw[0] = at4(w + 4 * (M == kGateUp || C::BN == kBlock ? 0 : wn * NJ * 16 / kBlock));
-    sw[1] = M == kGateUp ? at4(w + 4) : sw[0];
+    const uint32_t w = sc + wave * L::WSCALES + C::ADMA * 256;
+    sw[0] = at4(w + 16 * (M == kGateUp || C::BN == kBlock ? 0 : wn * NJ * 16 / kBlock));
+    sw[1] = M == kGateUp ? at4(w + 16) : sw[0];
   };
   wait_loads_barrier<(L::AHEAD - 2) * PER + EARLY>();
   read_scales();
@@ -501,15 +538,22 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
           cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
           ckt = ckt + 1 == nb ? 0 : ckt + 1;
           st = cslot * L::STAGE;
-          // (sums up to here are made here: the compiler would move them behind the branch, and keep all products)
+          if (ckt % kScaleGroup == 0) cgroup = cgroup + 1 == L::GROUPS ? 0 : cgroup + 1;
+          // The sums so far are made here: the compiler would move them behind the branches to come, and keep all
+          // products.  It counts these empty statements as wait states between a matrix instruction and the use of
+          // its result, so real ones follow (11 are needed).
 #pragma unroll
           for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int m = 0; m < NJ; ++m) asm volatile("" : "+v"(acc[i][m]));
+          asm volatile("s_nop 10");
           if (ikt == nb) {                                     // go on with the next tile's stages
             aim(cur, par ^ 1);
             ikt = 0;
+#pragma unroll
+            for (int u = 0; u <= C::ADMA; ++u) load_scales(0, gload, u);   // the slot after its predecessor's last group
           }
+          begin_stage();
           read_scales();
         }
         read_b((j + 2) % NJ);
@@ -547,6 +591,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
     for (int n = -LAG; n < 0; ++n) add(n);
 
     // ---- epilogue
+    const int elane = fresh_lane(), l16 = elane & 15, q = elane >> 4;
     const int n0 = it.chunk * OUTC;
     if constexpr (M == kGateUp) {
       uint32_t* mx = reinterpret_cast<uint32_t*>(lds + L::MAX);

@@ -25,28 +25,31 @@ template <int MI_, int NJ_, int WM_, int WN_>
 struct TileCfg {
   static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = i8::kLanes * NW;
   static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
-  static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;   // DMA instructions per wave and half
-  static_assert(ADMA >= 1 && ADMA <= 2 && BDMA >= 1, "a wave's rows take lanes 0 - 31 of a load of scales");
+  static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;   // a wave's 16-row blocks
+  static_assert(ADMA >= 1 && ADMA < 4 && BDMA >= 1, "a load of scales per stage: each 16 rows', the matrix's");
 };
 using TileWide = TileCfg<4, 8, 4, 2>;    // 256 rows x 256 weight rows
 using TileLow = TileCfg<4, 4, 2, 4>;     // 128 rows x 256
 using TileExact = TileCfg<4, 4, 4, 2>;   // 256 rows x 128
 
 constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile (TileLds)
+constexpr int kScaleGroup = 4;           // stages whose scales are loaded together
 template <class C, Mode M>
 struct TileLds {
-  static constexpr int A = C::BM * kHalf, B = C::BN * kHalf;   // bytes of half a stage
-  static constexpr int WSCALES = 144;                          // a wave's: 32 rows, two blocks of the matrix
-  static constexpr int STAGE = 2 * (A + B) + C::NW * WSCALES;
+  static constexpr int A = C::BM * kBlock, B = C::BN * kHalf;  // bytes of a stage's rows, of half a stage's weights
+  static constexpr int STAGE = A + 2 * B;
+  // scales of a group of stages: a wave's are its rows' (16 bytes each), then those of two blocks of the matrix
+  static constexpr int WSCALES = (16 * C::ADMA + 2) * 4 * kScaleGroup, SCALES = C::NW * WSCALES, GROUPS = 3;
   static constexpr int WROWS = 16 * C::ADMA * 4, ROWS = C::NW * WROWS;
-  static constexpr int FIXED = 2 * ROWS + (M == kGateUp ? C::WN * C::BM * 4 : 0) + 16;
+  static constexpr int FIXED = GROUPS * SCALES + 2 * ROWS + (M == kGateUp ? C::WN * C::BM * 4 : 0) + 16;
   static constexpr int plan_bytes(int G) { return 4 * C::NW + 8 * (G + 1); }
   static constexpr int kMostGroups = 2 * 512 + 256;
   static constexpr int STAGES = (i8::kLdsPerCu - FIXED - plan_bytes(kMostGroups)) / STAGE;
   static constexpr int AHEAD = STAGES;                         // stages requested before the first is multiplied
   static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
   static constexpr int RING = STAGES * STAGE, PLAN_ = RING + FIXED;
-  static constexpr int LIST = RING;                            // row list of two tiles
+  static constexpr int SCALE0 = RING;                          // scales of three groups of stages
+  static constexpr int LIST = RING + GROUPS * SCALES;                            // row list of two tiles
   static constexpr int MAX = LIST + 2 * ROWS;                  // kGateUp: largest magnitudes
   static constexpr int ZERO = PLAN_ - 16;                      // zeros
   static constexpr int PLAN = PLAN_;                    // sums over waves, tiles before each group, group offsets

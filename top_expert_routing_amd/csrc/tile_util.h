@@ -120,8 +120,15 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
   asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
-// The same for the lanes of `mask`, without a branch (which would end the block of instructions that the
-// compiler schedules).  Every lane of the wave takes part.
+// The same for the lanes of `mask`, from a wave-uniform address plus a lane's 32-bit offset or a lane's
+// address.  Every lane of the wave takes part.
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds, uint64_t mask) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32))) << 32 |
+                     static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+  asm volatile("s_nop 4\n\ts_mov_b64 exec, %2\n\tglobal_load_lds_dword %0, %1\n\ts_mov_b64 exec, -1"
+               : : "v"(off), "s"(u), "s"(mask), "{m0}"(lds) : "memory");
+}
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds, uint64_t mask) {
   asm volatile("s_nop 4\n\ts_mov_b64 exec, %1\n\tglobal_load_lds_dword %0, off\n\ts_mov_b64 exec, -1"
                : : "v"(g), "s"(mask), "{m0}"(lds) : "memory");
