@@ -21,10 +21,10 @@ int main() {
   char product[16];
   Sizes s;
   while (std::scanf("%15s %d %d %d %d %d %d", product, &s.n_rows, &s.E, &s.n_shared, &s.nseg, &s.K, &s.cols) == 7) {
-    const Mode m = !std::strcmp(product, "gate_up") ? kGateUp : !std::strcmp(product, "down") ? kDown : kLinear;
-    const Plan p = plan(m, !std::strcmp(product, "linear_f32"), s);
-    const char* names[] = {"stream", "tile_low", "tile_wide", "tile_exact"};
-    const Launch l = launch_of(moe::i8::Plan{moe::i8::Kernel::kStream, p.width, p.blocks});
+    const Plan p = std::strncmp(product, "linear", 6) ? ffn_plan(std::strcmp(product, "down") ? kGateUp : kDown, s)
+                                                      : linear_plan(!std::strcmp(product, "linear_f32"), s);
+    const char* names[] = {"few", "stream", "tile_low", "tile_wide", "tile_exact"};
+    const Launch l = launch_of(p);
     std::printf("%s %d %d %d %d\n", names[static_cast<int>(p.kernel)], p.width, p.blocks, l.x, l.y);
   }
   return 0;

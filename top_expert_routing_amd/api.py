@@ -686,21 +686,33 @@ def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
-def _code_out(q, s, rows, d, codes, like, index):
-    """Codes [*rows][d] and scales of a quantising call: the caller's, checked, or new ones."""
-    shape, dtype = (*rows, d), torch.float8_e4m3fn if codes == "fp8" else torch.int8
-    scales = (*rows, _blocks(d)) if codes == "fp8" else tuple(rows)
+def _code_out(q, s, shape, fp8, like, index):
+    """Codes of `shape` and scales of a quantising call: the caller's, checked, or new ones."""
+    dtype = torch.float8_e4m3fn if fp8 else torch.int8
+    scales = shape[:-1] + (_blocks(shape[-1]),) if fp8 else shape[:-1]
     if q is None:
         q = torch.empty(shape, dtype=dtype, device=index)
-    elif not _ok(q, index, dtype, shape):
+    elif not (q.dtype is dtype and q.shape == shape and q.get_device() == index and q.is_contiguous()):
         _out(q, "q", dtype, shape)
         _same_device(like, q=q)
     if s is None:
         s = torch.empty(scales, dtype=torch.float32, device=index)
-    elif not _ok(s, index, torch.float32, scales):
+    elif not (s.dtype is torch.float32 and s.shape == scales and s.get_device() == index and s.is_contiguous()):
         _out(s, "s", torch.float32, scales)
         _same_device(like, s=s)
     return q, s
+
+
+def _rows_of(x: torch.Tensor):
+    """GPU, shape and columns of rows x [..][d] of a supported type; the checks of _need."""
+    index, shape = x.get_device(), x.shape
+    if index < 0 or not shape or not x.is_contiguous():
+        _need(x, "x")
+        raise ValueError("x must have at least one dim")
+    return index, shape, shape[-1]
+
+
+_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -713,55 +725,64 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     norm is taken of it as stored there.  y has its own type or, if not given, x's; want_y=False leaves it
     out.  codes: None, "i8" (int8 codes and a scale per row, for grouped_linear_i8) or "fp8" (E4M3 codes and
     a scale for each 128 columns, for grouped_linear_fp8 and grouped_ffn_fp8)."""
-    _need(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dim")
-    if codes not in _lib.CODES:
+    index, shape, d = _rows_of(x)
+    code = _lib.CODES.get(codes)
+    if code is None:
         raise ValueError('codes must be None, "i8" or "fp8"')
-    if not want_y and (codes is None or y is not None):
-        raise ValueError("want_y=False goes with codes and without y")
-    if codes is None and (q is not None or s is not None):
-        raise ValueError("q and s go with codes")
-    index, shape = x.get_device(), x.shape
-    *rows, d = shape
-    if not _ok(weight, index, weight.dtype, (d,)):
+    # a small call's time is its host side: each tensor's checks in one expression, the messages where it fails
+    xt, wt, rt, yt, rp, op, yp, qp, sp = _TYPES.get(x.dtype), _TYPES.get(weight.dtype), 0, 0, None, None, None, None, None
+    if xt is None or wt is None:
+        _dtype_code(x)
+        _dtype_code(weight)
+    if not (weight.shape == (d,) and weight.get_device() == index and weight.is_contiguous()):
         _out(weight, "weight", weight.dtype, (d,))
         _same_device(x, weight=weight)
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out goes with residual")
-    else:
+    if residual is not None:
         if residual_out is None:
             residual_out = residual
-        for name, t in (("residual", residual), ("residual_out", residual_out)):
-            if not _ok(t, index, residual.dtype, shape):
+        rt = _TYPES.get(residual.dtype)
+        if rt is None:
+            _dtype_code(residual)
+        if not (residual.shape == shape and residual.get_device() == index and residual.is_contiguous() and
+                (residual_out is residual or (residual_out.dtype is residual.dtype and residual_out.shape == shape and
+                                              residual_out.get_device() == index and residual_out.is_contiguous()))):
+            for name, t in (("residual", residual), ("residual_out", residual_out)):
                 _out(t, name, residual.dtype, shape)
                 _same_device(x, **{name: t})
-    if y is None:
-        if want_y:
+        rp, op = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with residual")
+    if want_y:
+        if y is None:
             y = torch.empty(shape, dtype=x.dtype, device=index)
-    elif not _ok(y, index, y.dtype, shape):
-        _out(y, "y", y.dtype, shape)
-        _same_device(x, y=y)
-    T = x.numel() // d if d else 0
-    if codes is not None:
-        q, s = _code_out(q, s, rows, d, codes, x, index)
-    _call("moe_rmsnorm", index, _lib.load().moe_rmsnorm, x.data_ptr(), _dtype_code(x), _ptr(residual),
-          0 if residual is None else _dtype_code(residual), weight.data_ptr(), _dtype_code(weight), T, d, eps,
-          _ptr(residual_out), _ptr(y), 0 if y is None else _dtype_code(y), _lib.CODES[codes], _ptr(q), _ptr(s))
+        yt = _TYPES.get(y.dtype)
+        if yt is None:
+            _dtype_code(y)
+        if not (y.shape == shape and y.get_device() == index and y.is_contiguous()):
+            _out(y, "y", y.dtype, shape)
+            _same_device(x, y=y)
+        yp = y.data_ptr()
+    elif codes is None or y is not None:
+        raise ValueError("want_y=False goes with codes and without y")
+    if code:
+        q, s = _code_out(q, s, shape, code == 2, x, index)
+        qp, sp = q.data_ptr(), s.data_ptr()
+    elif q is not None or s is not None:
+        raise ValueError("q and s go with codes")
+    _call("moe_rmsnorm", index, _lib.load().moe_rmsnorm, x.data_ptr(), xt, rp, rt, weight.data_ptr(), wt,
+          x.numel() // d if d else 0, d, eps, op, yp, yt, code, qp, sp)
     return y, q, s
 
 
 def quantize_blocks_fp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None):
     """E4M3 codes [..][d] and fp32 scales [..][ceil(d / 128)] of the rows of x [..][d] (bf16 or fp32), a scale
     for each 128 columns: max|block| * fl(1/448), codes to the nearest (moe_quantize_blocks_fp8)."""
-    _need(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dim")
-    index = x.get_device()
-    *rows, d = x.shape
-    q, s = _code_out(q, s, rows, d, "fp8", x, index)
-    _call("moe_quantize_blocks_fp8", index, _lib.load().moe_quantize_blocks_fp8, x.data_ptr(), _dtype_code(x),
+    index, shape, d = _rows_of(x)
+    xt = _TYPES.get(x.dtype)
+    if xt is None:
+        _dtype_code(x)
+    q, s = _code_out(q, s, shape, True, x, index)
+    _call("moe_quantize_blocks_fp8", index, _lib.load().moe_quantize_blocks_fp8, x.data_ptr(), xt,
           x.numel() // d if d else 0, d, q.data_ptr(), s.data_ptr())
     return q, s
 
@@ -795,27 +816,31 @@ def grouped_linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, group_offsets: t
     E4M3 rows [n_x][K] with x_scale [n_x][ceil(K/128)], packed E4M3 matrices [E+S][O][K] (quantize_fp8_blocks,
     pack_fp8_codes) with w_scale [E+S][ceil(O/128)][ceil(K/128)]; bf16 or fp32 out (y's dtype, or `out_dtype`).
     E = 1 with offsets [0, N] is a plain linear map (moe_grouped_linear_fp8)."""
-    f8 = torch.float8_e4m3fn
-    _need(xq, "xq", f8, 2)
-    if w.dim() != 3:
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if xq.dtype is not f8 or xq.dim() != 2 or w.dim() != 3 or not xq.is_contiguous():
+        _need(xq, "xq", f8, 2)
         _need(w, "w", f8, 3)
-    n_x, K = xq.shape
-    G, O = E + n_shared, w.size(1)
-    index = xq.get_device()
+    (n_x, K), G, O, index = xq.shape, E + n_shared, w.size(1), xq.get_device()
+    if index < 0:
+        _need(xq, "xq")
     N = _i8_batch(xq, x_rows, group_offsets, E, n_shared, nseg)
-    _need_fp8_rows(xq, x_scale, index)
-    if not (_ok(w, index, f8, (G, O, K)) and _ok(w_scale, index, torch.float32, (G, _blocks(O), _blocks(K)))):
+    kb, ob = (K + 127) // FP8_BLOCK, (O + 127) // FP8_BLOCK
+    if not (x_scale.dtype is f32 and x_scale.shape == (n_x, kb) and x_scale.get_device() == index and
+            x_scale.is_contiguous() and w.dtype is f8 and w.shape == (G, O, K) and w.get_device() == index and
+            w.is_contiguous() and w_scale.dtype is f32 and w_scale.shape == (G, ob, kb) and
+            w_scale.get_device() == index and w_scale.is_contiguous()):
+        _out(x_scale, "x_scale", f32, (n_x, kb))
         _out(w, "w", f8, (G, O, K))
-        _out(w_scale, "w_scale", torch.float32, (G, _blocks(O), _blocks(K)))
-        _same_device(xq, w=w, w_scale=w_scale)
+        _out(w_scale, "w_scale", f32, (G, ob, kb))
+        _same_device(xq, x_scale=x_scale, w=w, w_scale=w_scale)
     if y is None:
         y = _new(N, O, out_dtype, index)
-    elif not _ok(y, index, y.dtype, (N, O)):
+    elif not (y.shape == (N, O) and y.get_device() == index and y.is_contiguous()):
         _out(y, "y", y.dtype, (N, O))
         _same_device(xq, y=y)
     _call("moe_grouped_linear_fp8", index, _lib.load().moe_grouped_linear_fp8, xq.data_ptr(), x_scale.data_ptr(),
-          _ptr(x_rows), n_x, group_offsets.data_ptr(), N, E, n_shared, nseg, K, O, w.data_ptr(), w_scale.data_ptr(),
-          _dtype_code(y), y.data_ptr())
+          None if x_rows is None else x_rows.data_ptr(), n_x, group_offsets.data_ptr(), N, E, n_shared, nseg, K, O,
+          w.data_ptr(), w_scale.data_ptr(), _dtype_code(y), y.data_ptr())
     return y
 
 

@@ -39,6 +39,7 @@ constexpr int kMaxGroups = 2 * 512 + 256;
 
 struct ProductArgs {
   const uint8_t* a;        // codes of the rows: [n_x][K]
+  const float* af;         // few_fp8<kDown>: the SwiGLU product [n_rows][K], in place of a and as
   const float* as;         // their scales: row r, block b at r * as_row + b * as_block
   size_t as_row, as_block;
   const uint8_t *w0, *w1;  // packed matrices [E+S][cols][K] (w1: up rows of kGateUp)
@@ -255,6 +256,154 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_fp8(ProductArgs p) {
       store4(static_cast<Out*>(p.out) + static_cast<size_t>(it.row(m)) * cols + n, v);
     }
   }
+}
+
+// ---- few rows: 16 columns per block, K split over its waves --------------------------
+// With few rows (one token's experts, a small dense batch) 128-column items are too few
+// to draw the weights through every CU, so an item is 16 columns (kGateUp: 16 gate and 16
+// up rows; 32 or 64 where there are many) of at most 16 rows and the eight waves split K by
+// whole blocks; their sums are joined through LDS in the order of the waves.
+// A block does not hold the columns that share a scale of the SwiGLU product, so kGateUp writes
+// that in fp32 (N * I * 4 bytes, at most 80 KiB here), and kDown's waves, each on whole blocks
+// of 128 columns, quantise it as they read it.
+constexpr int kFewBlocksHeld = 2;        // blocks of K in flight per wave
+constexpr int kSplit = kWavesS;
+
+template <int NC, Mode M, class Out>
+__global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_fp8(ProductArgs p) {
+  constexpr int NF = M == kGateUp ? 2 * NC : NC, U = kFewBlocksHeld;   // j < NC: gate or only, j >= NC: up
+  __shared__ f32x4 part[kSplit][NF][kWave];
+  const Item it = find_item(p, 16, p.cols / (16 * NC));
+  if (it.rows == 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+  const int l16 = lane & 15, q = lane >> 4;
+  const int K = p.K, cols = p.cols, nb = (K + kBlock - 1) / kBlock, ncb = (cols + kBlock - 1) / kBlock;
+  // this wave's blocks of K, dealt in equal runs
+  const int run = (nb + kSplit - 1) / kSplit;
+  const int b0 = min(nb, wave * run), b1 = min(nb, b0 + run);
+  const size_t rb = static_cast<size_t>(it.expert) * cols + it.chunk * 16 * NC;
+  const size_t sb = (static_cast<size_t>(it.expert) * ncb + it.chunk * 16 * NC / kBlock) * nb;
+  const uint8_t* wp[NF];                                    // wave-uniform; a lane's 16 bytes are its `lane`-th
+#pragma unroll
+  for (int j = 0; j < NF; ++j) wp[j] = (j < NC ? p.w0 : p.w1) + (rb + 16 * (j % NC)) * K;
+  // Loads without branches, so that the waits count them one by one: a half past K loads the matrix's last
+  // one (which its zeros of the rows multiply), a block past this wave's run what is not multiplied.
+  auto half_at = [&](int b, int h) MOE_INLINE { return static_cast<size_t>(min(b * kBlock + h * kHalf, K - kHalf)); };
+  uint4 w[U][NF][2];
+  auto load_w = [&](int b, int u) MOE_INLINE {
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[u][j][h] = reinterpret_cast<const uint4*>(wp[j] + half_at(b + u, h) * 16)[lane];
+  };
+  // this lane's row (lanes past the rows repeat the last one) and its 32 columns of each block: codes, kDown fp32
+  const int row = it.row(min(l16, it.rows - 1));
+  constexpr int PIECES = M == kDown ? 8 : 2;
+  uint4 x[U][PIECES];
+  float sx[U], sw[U][2];
+  const uint8_t* xr = nullptr;
+  const float* sr = nullptr;
+  auto load_x = [&](int b) MOE_INLINE {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int h = i / (PIECES / 2), k = i % (PIECES / 2);
+        x[u][i] = reinterpret_cast<const uint4*>(xr + half_at(b + u, h) * (PIECES / 2))[k];
+      }
+      const int at = min(b + u, nb - 1);
+      if constexpr (M != kDown) sx[u] = sr[at * p.as_block];
+      sw[u][0] = p.s0[sb + at];
+      if constexpr (M == kGateUp) sw[u][1] = p.s1[sb + at];
+    }
+  };
+  // A wave's loads return in order, so the first rows are asked for among the first weights
+  load_w(b0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (M == kDown) {
+    xr = reinterpret_cast<const uint8_t*>(p.af + static_cast<size_t>(row) * K + 16 * q);
+  } else {
+    const int src = src_row(p, row);
+    xr = p.a + static_cast<size_t>(src) * K + 16 * q;
+    sr = p.as + src * p.as_row;
+  }
+  load_x(b0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 1; u < U; ++u) load_w(b0, u);
+  __builtin_amdgcn_sched_barrier(0);
+
+  f32x4 acc[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = b0; b < b1; b += U) {
+    if (b != b0) {
+      load_x(b);
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_w(b, u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u >= b1) break;
+      const bool two = (b + u) * kBlock + kHalf < K;        // else the second half is past K: zeros
+      uint4 c[2];
+      if constexpr (M == kDown) {
+        float v[8][4];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f32x4 f = __builtin_bit_cast(f32x4, x[u][i]);
+          if (i >= 4 && !two) f = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v[i][r] = f[r];
+            m = max(m, abs_bits(f[r]));
+          }
+        }
+        const Fp8Scale bs = block_scale(max_over_q(m));
+        uint32_t d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = block_codes(v[i], bs.r);
+        c[0] = make_uint4(d[0], d[1], d[2], d[3]);
+        c[1] = make_uint4(d[4], d[5], d[6], d[7]);
+        sx[u] = bs.base;
+      } else {
+        c[0] = x[u][0];
+        c[1] = two ? x[u][1] : make_uint4(0, 0, 0, 0);
+      }
+      const Wide xw = widen(c);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const f32x4 t = mfma_wide(widen(w[u][j]), xw);
+        const float s = sx[u] * sw[u][M == kGateUp && j >= NC ? 1 : 0];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(t[r], s, acc[j][r]);
+      }
+    }
+  }
+  // join; wave j takes column block j
+#pragma unroll
+  for (int j = 0; j < NF; ++j) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave >= NC || l16 >= it.rows) return;
+  auto joined = [&](int j) MOE_INLINE {
+    f32x4 v = part[0][j][lane];
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) v += part[i][j][lane];
+    return v;
+  };
+  const int n = (it.chunk * NC + wave) * 16 + 4 * q;
+  const f32x4 g = joined(wave);
+  float v[4];
+  if constexpr (M == kGateUp) {
+    const f32x4 u = joined(NC + wave);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = silu_mul(g[r], u[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = g[r];
+  }
+  store4(static_cast<Out*>(p.out) + static_cast<size_t>(row) * cols + n, v);
 }
 
 // ---- large groups: LDS-tiled products ----------------------------------------------
@@ -684,11 +833,21 @@ void launch_tile(const ProductArgs& p, hipStream_t stream) {
 Sizes sizes_of(const ProductArgs& p) { return Sizes{p.n_rows, p.E, p.G - p.nseg * p.E, p.nseg, p.K, p.cols}; }
 
 template <Mode M, class Out>
-void launch_product(const ProductArgs& p, hipStream_t stream) {
+void launch_few(const ProductArgs& p, hipStream_t stream) {
+  const Plan plan = few_plan(M, sizes_of(p));
+  const Launch l = launch_of(plan);
+  const dim3 grid(l.x, l.y), block(kThreadsS);
+  if (plan.width == 1) hipLaunchKernelGGL((few_fp8<1, M, Out>), grid, block, 0, stream, p);
+  else if (plan.width == 2) hipLaunchKernelGGL((few_fp8<2, M, Out>), grid, block, 0, stream, p);
+  else if constexpr (M != kGateUp) hipLaunchKernelGGL((few_fp8<4, M, Out>), grid, block, 0, stream, p);
+}
+
+template <Mode M, class Out>
+void launch_many(const ProductArgs& p, hipStream_t stream) {
   constexpr bool exact = sizeof(Out) == 4;
-  const Plan plan = fp8::plan(M, exact, sizes_of(p));
+  const Plan plan = many_plan(M, exact, sizes_of(p));
   if (plan.kernel == Kernel::kStream) {
-    const Launch l = launch_of(i8::Plan{i8::Kernel::kStream, plan.width, plan.blocks});
+    const Launch l = launch_of(plan);
     const dim3 grid(l.x, l.y), block(kThreadsS);
     if (plan.width == 1) hipLaunchKernelGGL((stream_fp8<1, M, Out>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((stream_fp8<2, M, Out>), grid, block, 0, stream, p);
@@ -714,14 +873,14 @@ ProductArgs product_args(const GroupedFp8& g, int K, int cols) {
   return p;
 }
 
-// Workspace of the FFN: SwiGLU codes and block scales.
+// Workspace of the FFN: SwiGLU codes and block scales; of few rows, the product in fp32.
 struct FfnFp8Layout {
   size_t as, total;   // byte offsets (the codes start at 0)
 };
 FfnFp8Layout ffn_fp8_layout(int n_rows, int I) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   FfnFp8Layout L;
-  L.as = up(static_cast<size_t>(n_rows) * I);
+  L.as = up(static_cast<size_t>(n_rows) * I * (few_ffn(n_rows, I) ? 4 : 1));
   L.total = L.as + up(static_cast<size_t>((I + kBlock - 1) / kBlock) * n_rows * 4);
   return L;
 }
@@ -738,8 +897,13 @@ hipError_t launch_grouped_linear_fp8(const GroupedFp8& g, const uint8_t* xq, con
   p.w0 = w;
   p.s0 = ws;
   p.out = y;
-  if (bf16) launch_product<kLinear, uint16_t>(p, stream);
-  else launch_product<kLinear, float>(p, stream);
+  if (few_linear(sizes_of(p))) {
+    if (bf16) launch_few<kLinear, uint16_t>(p, stream);
+    else launch_few<kLinear, float>(p, stream);
+  } else {
+    if (bf16) launch_many<kLinear, uint16_t>(p, stream);
+    else launch_many<kLinear, float>(p, stream);
+  }
   return hipGetLastError();
 }
 
@@ -759,18 +923,22 @@ hipError_t launch_ffn_fp8(const FfnFp8Args& a, void* workspace, hipStream_t stre
   p.s1 = a.s_up;
   p.out = ws;
   p.out_scale = reinterpret_cast<float*>(ws + L.as);
-  launch_product<kGateUp, uint8_t>(p, stream);
+  const bool fp32 = few_ffn(a.g.n_rows, a.I);
+  if (fp32) launch_few<kGateUp, float>(p, stream);
+  else launch_many<kGateUp, uint8_t>(p, stream);
   ProductArgs h = product_args(a.g, a.I, a.d);
   h.x_rows = nullptr;                       // the SwiGLU product is in sorted order
   h.n_x = a.g.n_rows;
   h.a = ws;
+  h.af = reinterpret_cast<const float*>(ws);
   h.as = p.out_scale;
   h.as_row = 1;
   h.as_block = a.g.n_rows;
   h.w0 = a.w_down;
   h.s0 = a.s_down;
   h.out = a.h_sorted;
-  launch_product<kDown, uint16_t>(h, stream);
+  if (fp32) launch_few<kDown, uint16_t>(h, stream);
+  else launch_many<kDown, uint16_t>(h, stream);
   return hipGetLastError();
 }
 

@@ -11,7 +11,6 @@ using i8::kDown;
 using i8::kGateUp;
 using i8::kLinear;
 using i8::Launch;
-using i8::launch_of;
 using i8::max_m_tiles;
 using i8::Mode;
 using i8::Sizes;
@@ -59,23 +58,42 @@ struct TileLds {
   static_assert(AHEAD <= kTileMinStages, "a tile has more stages than are requested ahead");
 };
 
-enum class Kernel { kStream, kTileLow, kTileWide, kTileExact };
+enum class Kernel { kFew, kStream, kTileLow, kTileWide, kTileExact };
 struct Plan {
   Kernel kernel;
-  int width;    // stream_fp8: 16-row blocks of a tile
-  int blocks;   // stream_fp8: blocks of the launch (tile_fp8's walk a list)
+  int width;    // few_fp8: 16-column blocks of an item; stream_fp8: 16-row blocks of a tile
+  int blocks;   // few_fp8, stream_fp8: blocks of the launch (tile_fp8's walk a list)
 };
+inline Launch launch_of(const Plan& p) { return i8::launch_of(i8::Plan{i8::Kernel::kStream, p.width, p.blocks}); }
 
 constexpr int kTileMinAvg = 64, kWideMinAvg = 192;
 constexpr int kTileMinItems = 512;
 
-inline Plan plan(Mode m, bool exact, const Sizes& s) {
+// The FFN's products of few rows (both of them: the SwiGLU product is kept in fp32 then).
+inline bool few_ffn(int n_rows, int I) { return i8::few(n_rows, I); }
+inline bool few_linear(const Sizes& s) {
+  return static_cast<long long>(max_m_tiles(s, 16)) * (s.cols / 16) <= i8::kFewBlocksMost;
+}
+inline Plan few_plan(Mode m, const Sizes& s) {
+  const i8::Plan p = i8::plan_few(m, s);
+  return Plan{Kernel::kFew, p.width, p.blocks};
+}
+
+// exact: fp32 out
+inline Plan many_plan(Mode m, bool exact, const Sizes& s) {
   const int avg = s.n_rows / s.sequences();
   const long long area = static_cast<long long>(s.n_rows) * s.cols;
   if (avg > kTileMinAvg && area >= kTileMinItems * 64ll * 128 && s.K > (kTileMinStages - 1) * kBlock)
     return Plan{exact ? Kernel::kTileExact : avg >= kWideMinAvg ? Kernel::kTileWide : Kernel::kTileLow, 0, 0};
   const int nch = (s.cols + kBlock - 1) / kBlock, mf = i8::pick_mf(avg);
   return Plan{Kernel::kStream, mf, item_grid(max_m_tiles(s, 16 * mf), nch)};
+}
+
+inline Plan linear_plan(bool exact, const Sizes& s) { return few_linear(s) ? few_plan(kLinear, s) : many_plan(kLinear, exact, s); }
+
+// kGateUp: K = d, cols = I; kDown: K = I, cols = d.
+inline Plan ffn_plan(Mode m, const Sizes& s) {
+  return few_ffn(s.n_rows, m == kGateUp ? s.cols : s.K) ? few_plan(m, s) : many_plan(m, false, s);
 }
 
 }  // namespace fp8
