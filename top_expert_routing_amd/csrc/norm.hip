@@ -25,29 +25,32 @@ __device__ __forceinline__ uint32_t piece_max(const Piece& p) {
   return m;
 }
 
-// LANES threads per row; HELD pieces each (0: the row is read again for its outputs).
-template <int LANES, int HELD>
+enum Kind { kNone, kBf16, kF32 };
+
+// X: x's type, R: the residual's.  LANES threads per row; HELD pieces each (0: the row is read again for
+// its outputs).
+template <Kind X, Kind R, int LANES, int HELD>
 __global__ __launch_bounds__(kThreads) void rmsnorm(NormArgs a) {
-  constexpr int WAVES = LANES / kWave;
+  constexpr int WAVES = LANES / kWave, ROWS = kThreads / LANES;
   __shared__ float sums[kThreads / kWave];
   __shared__ uint32_t tops[kThreads / kWave];
-  const int t = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES, l = threadIdx.x % LANES;
-  if (LANES == kWave && t >= a.T) return;       // one row per block otherwise
-  const int d = a.d, nb = (d + kFp8Block - 1) / kFp8Block;
+  const int t = blockIdx.x * ROWS + threadIdx.x / LANES, l = threadIdx.x % LANES;
+  const bool there = ROWS == 1 || t < a.T;
+  if (WAVES == 1 && !there) return;             // rows of several wavefronts meet at a barrier
+  const int d = there ? a.d : 0, nb = (d + kFp8Block - 1) / kFp8Block;
   const size_t row = static_cast<size_t>(t) * d;
 
-  // r of a piece at column i: x, or the sum as it is stored
+  // r of a piece at column i: the sum as it is stored
   auto add = [&](Piece& p, const Piece& r, uint32_t i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) p.v[j] += r.v[j];
-    if (a.residual_bf16) {
+    if constexpr (R == kBf16) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) p.v[j] = bf16_to_f32(f32_to_bf16(p.v[j]));
     }
-    store8(a.residual_bf16, a.residual_out, row + i, p);
+    store8(R == kBf16, a.residual_out, row + i, p);
   };
-  auto weigh = [&](Piece& p, uint32_t i) {
-    const Piece w = load8(a.weight_bf16, a.weight, i);
+  auto weigh = [&](Piece& p, const Piece& w) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) p.v[j] *= w.v[j];
   };
@@ -62,40 +65,37 @@ __global__ __launch_bounds__(kThreads) void rmsnorm(NormArgs a) {
   float sum = 0.f;
   uint32_t top = 0;
   if constexpr (HELD > 0) {
+    // all of the row is asked for before the first sum is stored
+    RawPiece x[HELD], r[R != kNone ? HELD : 1], w[HELD];
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      const int i = (h * LANES + l) * 8;
+      if (i < d) {
+        x[h] = load8_raw(X == kBf16, a.x, row + i);
+        if constexpr (R != kNone) r[h] = load8_raw(R == kBf16, a.residual, row + i);
+        w[h] = load8_raw(a.weight_bf16, a.weight, i);
+      }
+    }
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
       const int i = (h * LANES + l) * 8;
       held[h] = Piece{};
-      if (i < d) held[h] = load8(a.x_bf16, a.x, row + i);
-    }
-    if (a.residual) {                           // all of it is asked for before the first sum is stored
-      Piece r[HELD];
-#pragma unroll
-      for (int h = 0; h < HELD; ++h) {
-        const int i = (h * LANES + l) * 8;
-        if (i < d) r[h] = load8(a.residual_bf16, a.residual, row + i);
+      if (i < d) {
+        held[h] = unpack8(X == kBf16, x[h]);
+        if constexpr (R != kNone) add(held[h], unpack8(R == kBf16, r[h]), i);
+        sum += squares(held[h]);
+        weigh(held[h], a.weight_bf16 ? unpack8(true, w[h]) : unpack8(false, w[h]));
       }
-#pragma unroll
-      for (int h = 0; h < HELD; ++h) {
-        const int i = (h * LANES + l) * 8;
-        if (i < d) add(held[h], r[h], i);
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < HELD; ++h) {
-      const int i = (h * LANES + l) * 8;
-      sum += squares(held[h]);
-      if (i < d) weigh(held[h], i);
       if (a.code == kCodeI8) top = max(top, piece_max(held[h]));
     }
   } else {
     // unsigned: the last step of a row next to 2^31 values passes int32
     for (uint32_t i = l * 8; i < static_cast<uint32_t>(d); i += LANES * 8) {
-      Piece p = load8(a.x_bf16, a.x, row + i);
-      if (a.residual) add(p, load8(a.residual_bf16, a.residual, row + i), i);
+      Piece p = load8<X == kBf16>(a.x, row + i);
+      if constexpr (R != kNone) add(p, load8<R == kBf16>(a.residual, row + i), i);
       sum += squares(p);
       if (a.code == kCodeI8) {
-        weigh(p, i);
+        weigh(p, unpack8(a.weight_bf16, load8_raw(a.weight_bf16, a.weight, i)));
         top = max(top, piece_max(p));
       }
     }
@@ -111,12 +111,14 @@ __global__ __launch_bounds__(kThreads) void rmsnorm(NormArgs a) {
       tops[threadIdx.x >> 6] = top;
     }
     __syncthreads();
+    const int w0 = threadIdx.x / LANES * WAVES;
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      sum += sums[w];
-      top = max(top, tops[w]);
+      sum += sums[w0 + w];
+      top = max(top, tops[w0 + w]);
     }
+    if (!there) return;
   }
   // a row that is not finite, or whose sum of squares is not: NaN everywhere
   const float mean = sum / static_cast<float>(d);
@@ -150,8 +152,9 @@ __global__ __launch_bounds__(kThreads) void rmsnorm(NormArgs a) {
       const bool in = i < static_cast<uint32_t>(d);
       Piece p{};
       if (in) {
-        p = a.residual ? load8(a.residual_bf16, a.residual_out, row + i) : load8(a.x_bf16, a.x, row + i);
-        weigh(p, i);
+        if constexpr (R != kNone) p = load8<R == kBf16>(a.residual_out, row + i);
+        else p = load8<X == kBf16>(a.x, row + i);
+        weigh(p, unpack8(a.weight_bf16, load8_raw(a.weight_bf16, a.weight, i)));
       }
       finish(p, static_cast<int>(i), in);
     }
@@ -159,20 +162,19 @@ __global__ __launch_bounds__(kThreads) void rmsnorm(NormArgs a) {
   if (a.code == kCodeI8 && l == 0) a.s[t] = qs.scale * rstd;
 }
 
+template <Kind X, Kind R>
 void launch_norm_rows(const NormArgs& a, hipStream_t stream) {
   const dim3 block(kThreads);
-  if (a.d <= kWave * 8) {
-    const dim3 grid((a.T + kThreads / kWave - 1) / (kThreads / kWave));
-    hipLaunchKernelGGL((rmsnorm<kWave, 1>), grid, block, 0, stream, a);
-    return;
-  }
-  const int pieces = (a.d / 8 + kThreads - 1) / kThreads;
-  const dim3 grid(a.T);
-  if (pieces <= 1) hipLaunchKernelGGL((rmsnorm<kThreads, 1>), grid, block, 0, stream, a);
-  else if (pieces <= 2) hipLaunchKernelGGL((rmsnorm<kThreads, 2>), grid, block, 0, stream, a);
-  else if (pieces <= 4) hipLaunchKernelGGL((rmsnorm<kThreads, 4>), grid, block, 0, stream, a);
-  else if (pieces <= kMaxHeld) hipLaunchKernelGGL((rmsnorm<kThreads, kMaxHeld>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((rmsnorm<kThreads, 0>), grid, block, 0, stream, a);
+  const int pieces = a.d / 8;
+  auto grid = [&](int lanes) { return dim3((static_cast<unsigned>(a.T) * lanes + kThreads - 1) / kThreads); };
+  if (pieces <= 64) hipLaunchKernelGGL((rmsnorm<X, R, 64, 1>), grid(64), block, 0, stream, a);
+  else if (pieces <= 128) hipLaunchKernelGGL((rmsnorm<X, R, 128, 1>), grid(128), block, 0, stream, a);
+  else if (pieces <= 256) hipLaunchKernelGGL((rmsnorm<X, R, 256, 1>), grid(256), block, 0, stream, a);
+  else if (pieces <= 384) hipLaunchKernelGGL((rmsnorm<X, R, 128, 3>), grid(128), block, 0, stream, a);
+  else if (pieces <= 512) hipLaunchKernelGGL((rmsnorm<X, R, 256, 2>), grid(256), block, 0, stream, a);
+  else if (pieces <= 1024) hipLaunchKernelGGL((rmsnorm<X, R, 256, 4>), grid(256), block, 0, stream, a);
+  else if (pieces <= 2048) hipLaunchKernelGGL((rmsnorm<X, R, 256, kMaxHeld>), grid(256), block, 0, stream, a);
+  else hipLaunchKernelGGL((rmsnorm<X, R, 256, 0>), grid(256), block, 0, stream, a);
 }
 
 // ---- quantiser ------------------------------------------------------------------------
@@ -214,7 +216,16 @@ hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t stream) {
       a.q = args.q + at;
       a.s = args.s + static_cast<size_t>(t) * (a.code == kCodeFp8 ? nb : 1);
     }
-    launch_norm_rows(a, stream);
+    const Kind r = !a.residual ? kNone : a.residual_bf16 ? kBf16 : kF32;
+    if (a.x_bf16) {
+      if (r == kNone) launch_norm_rows<kBf16, kNone>(a, stream);
+      else if (r == kBf16) launch_norm_rows<kBf16, kBf16>(a, stream);
+      else launch_norm_rows<kBf16, kF32>(a, stream);
+    } else {
+      if (r == kNone) launch_norm_rows<kF32, kNone>(a, stream);
+      else if (r == kBf16) launch_norm_rows<kF32, kBf16>(a, stream);
+      else launch_norm_rows<kF32, kF32>(a, stream);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.T < kMost) break;                     // t + kMost may pass int32

@@ -28,8 +28,28 @@ __device__ __forceinline__ Piece load8(const void* x, size_t i) {
   return p;
 }
 
-__device__ __forceinline__ Piece load8(bool bf16, const void* x, size_t i) {
-  return bf16 ? load8<true>(x, i) : load8<false>(x, i);
+// The same in two steps, so that many pieces are asked for before the first is waited for.
+struct RawPiece {
+  uint4 u[2];              // bf16: the first only
+};
+__device__ __forceinline__ RawPiece load8_raw(bool bf16, const void* x, size_t i) {
+  RawPiece r;
+  if (bf16) {
+    r.u[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
+    r.u[1] = r.u[0];
+  } else {
+    r.u[0] = *reinterpret_cast<const uint4*>(static_cast<const float*>(x) + i);
+    r.u[1] = *reinterpret_cast<const uint4*>(static_cast<const float*>(x) + i + 4);
+  }
+  return r;
+}
+__device__ __forceinline__ Piece unpack8(bool bf16, const RawPiece& r) {
+  const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[1].x, r.u[1].y, r.u[1].z, r.u[1].w};
+  Piece p;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    p.v[j] = __uint_as_float(bf16 ? (j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16) : w[j]);
+  return p;
 }
 
 __device__ __forceinline__ void store8(bool bf16, void* y, size_t i, const Piece& p) {
