@@ -588,7 +588,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
     if (u == 0) gload = gload + 1 == L::GROUPS ? 0 : gload + 1;
     load_scales(ikt / kScaleGroup + 1, gload, u);
   };
-  constexpr int EARLY = PER * 2 / (NJ - 1);                    // loads of a stage that are requested in its step's last two passes
+  constexpr int EARLY = PER / 2;                    // loads of a stage that are requested in its step's last two passes
 #pragma unroll 1
   for (int s = 0; s < L::AHEAD - 1; ++s) {                     // nb >= AHEAD (kTileMinStages)
     begin_stage();
@@ -722,14 +722,15 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
           if (j == NJ - 1) read_a(i);
           add(j * MI + i - LAG);
         }
+        constexpr int OTHERS = NJ / 4;
         // a stage's loads: the first EARLY in the last two passes, the others in all but the last three
         if (j >= NJ - 2) {
 #pragma unroll
           for (int l = (j - (NJ - 2)) * EARLY / 2; l < (j - (NJ - 3)) * EARLY / 2; ++l) load(l);
-        } else if (j < NJ - 3) {
+        } else if (j < OTHERS) {
 #pragma unroll
-          for (int l = EARLY + j * (PER - EARLY) / (NJ - 3); l < EARLY + (j + 1) * (PER - EARLY) / (NJ - 3); ++l) load(l);
-          if (j == NJ - 4) loaded();
+          for (int l = EARLY + j * (PER - EARLY) / OTHERS; l < EARLY + (j + 1) * (PER - EARLY) / OTHERS; ++l) load(l);
+          if (j == OTHERS - 1) loaded();
         }
         __builtin_amdgcn_sched_barrier(0);
       }
