@@ -45,4 +45,4 @@ def ffn(n_rows, E, n_shared, nseg, d, I):
 
 def on_codes(kernel):
     """Whether a kernel multiplies on the FP8 matrix instructions (fp8_oracle.cut)."""
-    return kernel in ("tile_low", "tile_wide")
+    return kernel == "tile_codes"

@@ -9,12 +9,9 @@
 using namespace moe::fp8;
 
 // every layout that the kernels use: its static_asserts hold
-template struct moe::fp8::TileLds<TileWide, kLinear>;
-template struct moe::fp8::TileLds<TileWide, kGateUp>;
-template struct moe::fp8::TileLds<TileWide, kDown>;
-template struct moe::fp8::TileLds<TileLow, kLinear>;
-template struct moe::fp8::TileLds<TileLow, kGateUp>;
-template struct moe::fp8::TileLds<TileLow, kDown>;
+template struct moe::fp8::TileLds<TileCodes, kLinear>;
+template struct moe::fp8::TileLds<TileCodes, kGateUp>;
+template struct moe::fp8::TileLds<TileCodes, kDown>;
 template struct moe::fp8::TileLds<TileExact, kLinear>;
 
 int main() {
@@ -23,7 +20,7 @@ int main() {
   while (std::scanf("%15s %d %d %d %d %d %d", product, &s.n_rows, &s.E, &s.n_shared, &s.nseg, &s.K, &s.cols) == 7) {
     const Plan p = std::strncmp(product, "linear", 6) ? ffn_plan(std::strcmp(product, "down") ? kGateUp : kDown, s)
                                                       : linear_plan(!std::strcmp(product, "linear_f32"), s);
-    const char* names[] = {"few", "stream", "tile_low", "tile_wide", "tile_exact"};
+    const char* names[] = {"few", "stream", "tile_codes", "tile_exact"};
     const Launch l = launch_of(p);
     std::printf("%s %d %d %d %d\n", names[static_cast<int>(p.kernel)], p.width, p.blocks, l.x, l.y);
   }

@@ -9,10 +9,11 @@
 // A block's sum starts at zero in the matrix instructions, and one fma with sx * sw adds it to the
 // running fp32 sum.
 //
-// The codes are widened to bf16, which has every E4M3 value, and multiplied by
-// v_mfma_f32_16x16x32_bf16, because the FP8 matrix instructions do not add in fp32: of each 8 columns
-// of K they cut every product to a multiple of 2^(e - 13), e the exponent of the largest of the eight
-// (measured: 1.5e-5 to 5e-5 of a sum in the 2-norm).
+// The FP8 matrix instructions do not add in fp32: of each 8 columns of K they cut every product to a multiple of
+// 2^(e - 13), e the exponent of the largest of the eight (measured: 1.5e-5 to 5e-5 of a sum in the 2-norm).
+// tile_fp8 uses them where the result is rounded to bf16 (2^-9 of a value and more), at twice the rate.  Where it is
+// fp32, and in the kernels of fewer rows, which wait for memory, the codes are widened to bf16, which has every
+// E4M3 value, and multiplied by v_mfma_f32_16x16x32_bf16.
 //
 // Which of the 128 columns a lane holds does not matter as long as both operands agree:
 // lane 16 q + r holds columns 16 q .. 16 q + 15 and 64 + 16 q .. 64 + 16 q + 15 of row r, which
@@ -35,7 +36,6 @@ using namespace fp8;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 static_assert(kBlock == kFp8Block && i8::kLanes == kWave, "one block size, one wavefront");
-constexpr int kMaxGroups = 2 * 512 + 256;
 
 struct ProductArgs {
   const uint8_t* a;        // codes of the rows: [n_x][K]
@@ -409,19 +409,30 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_fp8(ProductArg
 // ---- large groups: LDS-tiled products ----------------------------------------------
 // A persistent block (one per CU) walks its list of tiles: BM rows x BN weight rows
 // (kGateUp: 128 gate and the same 128 up rows).  K advances 128 codes a stage through a
-// ring of LDS stages that LDS-DMA loads fill ahead; the stages of all tiles form one
-// stream, so the next tile's first stages load while this one finishes.
+// ring of LDS stages; the stages of all tiles form one stream, so the next tile's first
+// stages load while this one finishes.
+// Some waves multiply and four load.  A wave that requests an LDS-DMA load waits while the CU's address unit is
+// busy, and it is busy most of the time: where all waves did both, a tile's time was the sum of the two (FFN of
+// 96 rows for each of 64 experts, 2048 x 1024, 123 us with tiles of this size, 109 with waves that load; of 256 rows 238 / 195;
+// 8192 rows x 8192 -> 4096 265 us with tiles of 256 x 256, 270 with these of 128 x 256).
+// What bounds it: at 8192 x 8192 -> 4096 the loads alone take 214 us (159 from a warm L2), the matrix instructions alone 134,
+// those with their LDS reads 234.
+// EXACT (fp32 out) multiplies codes widened to bf16, at half the rate and with 16 conversions for each operand: four waves of
+// 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 166 us instead of 174).
 //   * rows: 128 bytes of a row per stage, eight 16-byte pieces; piece c of row r lies at slot
 //     c ^ ((r / 2) % 8), so that the 16 rows of an operand read hit different banks.  A DMA instruction
-//     fills 8 rows (lane -> row lane / 8, slot lane % 8): whole cache lines, whose number bounds the loads.
+//     fills 8 rows (lane -> row lane / 8, slot lane % 8).
 //   * weights: a packed block (16 rows x 64 codes, 1 KiB) is copied as it is.
 //   * scales: those of four stages together, since a row's lie in one cache line: a 4-byte load for
-//     each 16 of a wave's rows (lane 4 r + k: row r, stage k), and one for the matrix's (kGateUp: gate's and
-//     up's, else those of the tile's two blocks of 128 columns), one load per stage.
+//     each 16 rows (lane 4 r + k: row r, stage k), and one for the matrix's (kGateUp: gate's and up's,
+//     else those of the tile's two blocks of 128 columns).
 //   * the row list comes by DMA too, a tile ahead, because a load that the compiler sees would
 //     make it wait for everything in flight.
-// Waves: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave, so the
+// Barrier s, two passes before the end of step s (the multiplication of stage s), says that stage s + 1 has
+// arrived and that stage s has been read: stage s + STAGES takes its place.
+// Waves that multiply: WM x WN, each MI x NJ blocks of 16x16; the 16-row blocks of the waves interleave, so the
 // rows of a partial tile spread over them.
+
 // The lane's number, made anew: what is computed from it outside the K loop does not stay in registers through it.
 __device__ __forceinline__ int fresh_lane() {
   int l;
@@ -430,20 +441,19 @@ __device__ __forceinline__ int fresh_lane() {
 }
 
 template <class C, Mode M, bool EXACT, class Out>
-__global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
+__global__ __launch_bounds__(C::NT, (C::NW + kLoaders) / 4) void tile_fp8(ProductArgs p) {
   using L = TileLds<C, M>;
-  constexpr int MI = C::MI, NJ = C::NJ, WM = C::WM, WN = C::WN, NW = C::NW, NT = C::NT, BM = C::BM;
+  constexpr int MI = C::MI, NJ = C::NJ, WM = C::WM, WN = C::WN, NW = C::NW, NT = C::NT, BM = C::BM, STAGES = C::STAGES;
   constexpr int OUTC = M == kGateUp ? C::BN / 2 : C::BN;
-  constexpr int GPT = (kMaxGroups + NT - 1) / NT;
+  constexpr int GPT = (kTileMostGroups + NT - 1) / NT;
   constexpr int kPanel = 4;                                    // column chunks that follow each other per m-tile
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int* wsum = reinterpret_cast<int*>(lds + L::PLAN);
-  int* before = wsum + NW;                                     // m-tiles before group g
+  int* before = wsum + NW + kLoaders;                          // m-tiles before group g
   int* offs = before + p.G + 1;
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
   const int K = p.K, cols = p.cols;
-  const int nb = (K + kBlock - 1) / kBlock, ncb = (cols + kBlock - 1) / kBlock;
+  const int nb = (K + kBlock - 1) / kBlock, ncb = (cols + kBlock - 1) / kBlock, halves = K / kHalf;
 
   for (int g = tid; g <= p.G; g += NT) offs[g] = p.offs[g];
   if (tid < 4) reinterpret_cast<uint32_t*>(lds + L::ZERO)[tid] = 0;
@@ -496,116 +506,128 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
                               BM, p.E, p.nseg));
   };
 
-  // ---- the loads, STAGES - 1 stages ahead of the products
-  const uint32_t lds0 = lds_address(lds);
-  const int halves = K / kHalf;
-  uint32_t ao[2 * C::ADMA];                                    // of the tile being loaded: this lane's bytes from p.a,
-  uint32_t so[C::ADMA];                                        // its rows' scales, in floats from p.as,
-  const uint8_t* bp[C::BDMA];                                  // the weights (wave-uniform),
-  const float *wp0, *wp1;                                      // the matrix's scales (wave-uniform),
-  const uint32_t last = static_cast<uint32_t>(p.n_x) * K - 16; // no row piece starts later: a short last stage's pieces past K
+  // ---- the waves that load ------------------------------------------------------------
+  if (wave >= NW) {
+    constexpr int AL = C::AL, BL = C::BL, SL = C::SL, PER = AL + 2 * BL;   // PER: loads of a stage's codes
+    const int w = wave - NW;                                   // rows 8 AL w .., weight blocks BL w .. of a tile are this wave's
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t as_row = static_cast<uint32_t>(p.as_row), as_block = static_cast<uint32_t>(p.as_block);
+    const uint32_t last = static_cast<uint32_t>(p.n_x) * K - 16;   // no row piece starts later: a short last stage's pieces past K
                                                                // are another row's, and not used (read_a)
-  // lane 16 i + r of a wave has row r of the 16 rows of its block i, so wave w's rows are the w-th 16 * ADMA of ROWS
-  const uint32_t as_row = static_cast<uint32_t>(p.as_row), as_block = static_cast<uint32_t>(p.as_block);
-  auto load_list = [&](const Item& it, int parity) MOE_INLINE {
-    const int lane = fresh_lane();
-    if (p.x_rows && lane < 16 * C::ADMA)
-      dma4(p.x_rows + it.row(min(16 * (wave + NW * (lane >> 4)) + (lane & 15), it.rows - 1)), lds0 + L::LIST + parity * L::ROWS + wave * L::WROWS);
-  };
-  // Sources of a tile whose row list has arrived.
-  auto aim = [&](const Item& it, int parity) MOE_INLINE {
-    const int lane = fresh_lane();
-    const int* list = reinterpret_cast<const int*>(lds + L::LIST + parity * L::ROWS + wave * L::WROWS);
-    auto src = [&](int r, int slot) MOE_INLINE {
-      return p.x_rows ? min(max(list[slot], 0), p.n_x - 1) : it.row(min(r, it.rows - 1));
+    uint32_t ao[AL];                                           // of the tile being loaded: this lane's bytes from p.a,
+    uint32_t so[SL];                                           // its rows' scales, in floats from p.as,
+    const uint8_t* bp[BL];                                     // the weights (wave-uniform),
+    const float *wp0, *wp1;                                    // the matrix's scales (wave-uniform)
+    const uint32_t list0 = lds0 + L::LIST + w * 8 * AL * 4;
+    auto load_list = [&](const Item& it, int parity) MOE_INLINE {
+      if (p.x_rows && lane < 8 * AL)
+        dma4(p.x_rows + it.row(min(8 * AL * w + lane, it.rows - 1)), list0 + parity * BM * 4);
     };
+    // Sources of a tile whose row list has arrived.
+    auto aim = [&](const Item& it, int parity) MOE_INLINE {
+      const int* list = reinterpret_cast<const int*>(lds + L::LIST + (parity * BM + w * 8 * AL) * 4);
+      auto src = [&](int r) MOE_INLINE {                       // of this wave's rows
+        return p.x_rows ? min(max(list[r], 0), p.n_x - 1) : it.row(min(8 * AL * w + r, it.rows - 1));
+      };
 #pragma unroll
-    for (int i = 0; i < 2 * C::ADMA; ++i) {
-      const int t = 8 * (i & 1) + (lane >> 3);                 // row of the 16
-      ao[i] = static_cast<uint32_t>(src(16 * (wave + NW * (i >> 1)) + t, 16 * (i >> 1) + t)) * K + 16 * ((lane & 7) ^ ((t >> 1) & 7));
+      for (int i = 0; i < AL; ++i) {
+        const int r = 8 * i + (lane >> 3);
+        ao[i] = static_cast<uint32_t>(src(r)) * K + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+      }
+#pragma unroll
+      for (int i = 0; i < SL; ++i) so[i] = src(16 * i + (lane >> 2)) * as_row + (lane & 3) * as_block;
+      const int n0 = it.chunk * OUTC;
+      const size_t e0 = static_cast<size_t>(it.expert) * cols;
+#pragma unroll
+      for (int i = 0; i < BL; ++i) {
+        const int b = w * BL + i;                              // 16-row block of the tile
+        const bool up = M == kGateUp && b >= C::BN / 32;
+        const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
+        bp[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
+      }
+      const size_t sb = static_cast<size_t>(it.expert) * ncb;
+      const int cb = M == kGateUp ? it.chunk : it.chunk * (OUTC / kBlock);
+      wp0 = p.s0 + (sb + cb) * nb;
+      wp1 = M == kGateUp ? p.s1 + (sb + cb) * nb : p.s0 + (sb + min(cb + 1, ncb - 1)) * nb;
+    };
+    // Part u of a group's scales: 16 of this wave's rows, or the matrix's; lanes past K's blocks take no part.
+    auto load_scales = [&](int group, int slot, int u) MOE_INLINE {
+      const int left = nb - group * kScaleGroup;
+      const uint64_t four = left >= kScaleGroup ? 15 : left > 0 ? (1 << left) - 1 : 0;
+      const uint32_t to = lds0 + L::SCALE0 + slot * L::SCALES;
+      if (u < SL) {
+        dma4(p.as, (so[SL > 1 && u == 1 ? SL - 1 : 0] + group * kScaleGroup * as_block) * 4, to + (w * SL + u) * 256,
+             four * 0x1111111111111111ull);
+      } else if (u == SL) {
+        dma4((lane & 4 ? wp1 : wp0) + group * kScaleGroup + (lane & 3), to + L::WSCALE, w == 0 ? four * 0x11ull : 0);
+      }
+    };
+    int tile = 0, ikt = 0, islot = 0, gslot = -1;              // the stage requested next: tile, number in it, ring slot; its group's slot
+    auto request = [&]() MOE_INLINE {
+      if (ikt == nb) {                                         // go on with the next tile
+        ikt = 0;
+        ++tile;
+        aim(item_of(tile), tile & 1);
+        if (tile + 1 < n_my) load_list(item_of(tile + 1), (tile + 1) & 1);
+      }
+      // A group's scales are requested with the second and later stages of the group before, a tile's first group's with
+      // its first stage.  At most two groups (three with four stages) lie between what is requested and what is read.
+      auto after = [](int g) MOE_INLINE { return g + 1 == L::GROUPS ? 0 : g + 1; };
+      const int u = ikt % kScaleGroup;
+      if (u == 0) gslot = after(gslot);
+      if (ikt == 0) {
+#pragma unroll
+        for (int i = 0; i <= SL; ++i) load_scales(0, gslot, i);
+      } else if (u > 0) {
+        load_scales(ikt / kScaleGroup + 1, after(gslot), u - 1);
+      }
+      const uint32_t to = lds0 + islot * L::STAGE, k = ikt * kBlock;
+#pragma unroll
+      for (int i = 0; i < AL; ++i) dma16(p.a + k, min(ao[i], last - k), to + (w * AL + i) * 1024);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kt = min(2 * ikt + h, halves - 1);           // the half past K: the last one again (read_a)
+#pragma unroll
+        for (int i = 0; i < BL; ++i)
+          dma16(bp[i] + static_cast<size_t>(kt) * 1024, lane * 16, to + L::A + h * L::B + (w * BL + i) * 1024);
+      }
+      islot = islot + 1 == STAGES ? 0 : islot + 1;
+      ++ikt;
+    };
+    load_list(item_of(0), 0);
+    if (n_my > 1) load_list(item_of(1), 1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    aim(item_of(0), 0);
+    const int total = n_my * nb;                               // at least kTileMinStages
+    const int ahead = min(STAGES, total);
+    for (int s = 0; s < ahead; ++s) request();
+    if (ahead == STAGES) wait_loads<(STAGES - 1) * PER>();
+    else wait_loads<0>();
+    barrier();                                                 // stage 0 has arrived
+    int to_end = nb;                                           // steps of the tile that is multiplied
+    for (int s = 0; s < total; ++s) {
+      if (s + STAGES <= total) wait_loads<(STAGES - 2) * PER>();
+      else wait_loads<0>();
+      barrier();                                               // barrier s
+      if (s + STAGES < total) request();
+      if (--to_end == 0) {
+        to_end = nb;
+        if (M == kGateUp) barrier();                           // the epilogue's
+      }
     }
-#pragma unroll
-    for (int i = 0; i < C::ADMA; ++i)
-      so[i] = src(16 * (wave + NW * i) + (lane >> 2), 16 * i + (lane >> 2)) * as_row + (lane & 3) * as_block;
-    const int n0 = it.chunk * OUTC;
-    const size_t e0 = static_cast<size_t>(it.expert) * cols;
-#pragma unroll
-    for (int i = 0; i < C::BDMA; ++i) {
-      const int b = wave + NW * i;                             // 16-row block of the tile
-      const bool up = M == kGateUp && b >= C::BN / 32;
-      const int n = min(n0 + 16 * (up ? b - C::BN / 32 : b), cols - 16);   // past the columns: read, never stored
-      bp[i] = (up ? p.w1 : p.w0) + (e0 + n) * K;
-    }
-    const size_t sb = static_cast<size_t>(it.expert) * ncb;
-    wp0 = p.s0 + (sb + (M == kGateUp ? it.chunk : it.chunk * (OUTC / kBlock))) * nb;
-    wp1 = M == kGateUp ? p.s1 + (sb + it.chunk) * nb : p.s0 + (sb + min(it.chunk * (OUTC / kBlock) + 1, ncb - 1)) * nb;
-  };
-  int ikt = 0, islot = 0;                                      // the stage requested next: of its tile, ring slot
-  int gload = 0;                                               // slot of the group of scales requested last
-  // Part u of a group's scales: 16 of the rows', the matrix's; lanes past K's blocks take no part.
-  auto load_scales = [&](int group, int slot, int u) MOE_INLINE {
-    const int left = nb - group * kScaleGroup;
-    const uint64_t four = left >= kScaleGroup ? 15 : left > 0 ? (1 << left) - 1 : 0;
-    const uint32_t to = lds0 + L::SCALE0 + slot * L::SCALES + wave * L::WSCALES;
-    if (u < C::ADMA) {
-      uint32_t o = so[0];
-#pragma unroll
-      for (int i = 1; i < C::ADMA; ++i) o = u == i ? so[i] : o;
-      dma4(p.as, (o + group * kScaleGroup * as_block) * 4, to + u * 256, four * 0x1111111111111111ull);
-    } else if (u == C::ADMA) {
-      const int lane = fresh_lane();
-      dma4((lane & 4 ? wp1 : wp0) + group * kScaleGroup + (lane & 3), to + u * 256, four * 0x11ull);
-    }
-  };
-  constexpr int PER = 2 * (C::ADMA + C::BDMA);                 // loads of a stage's codes per wave
-  auto load = [&](int i) MOE_INLINE {                          // the i-th of them
-    const uint32_t to = lds0 + islot * L::STAGE;
-    if (i < 2 * C::ADMA) {
-      const uint32_t k = ikt * kBlock;
-      dma16(p.a + k, min(ao[i], last - k), to + ((i >> 1) * NW + wave) * 2048 + (i & 1) * 1024);
-    } else {
-      const int h = (i - 2 * C::ADMA) / C::BDMA, n = (i - 2 * C::ADMA) % C::BDMA;
-      const int kt = min(2 * ikt + h, halves - 1);             // the half past K: the last one again (read_a)
-      dma16(bp[n] + static_cast<size_t>(kt) * 1024, lane * 16, to + L::A + h * L::B + (n * NW + wave) * 1024);
-    }
-  };
-  auto loaded = [&]() MOE_INLINE {
-    islot = islot + 1 == L::STAGES ? 0 : islot + 1;
-    ++ikt;
-  };
-  Item cur = item_of(0), nxt = n_my > 1 ? item_of(1) : cur;
-  load_list(cur, 0);
-  load_list(nxt, 1);
-  wait_loads_barrier<0>();
-  aim(cur, 0);
-#pragma unroll
-  for (int u = 0; u <= C::ADMA; ++u) load_scales(0, 0, u);
-  // Where a stage's loads begin: its part of the scales of the group after its own.  Three slots are enough with
-  // two stages ahead: the group that a slot held was read to its end when a stage of the third one begins.
-  static_assert(L::AHEAD == 2, "three groups of scales");
-  auto begin_stage = [&]() MOE_INLINE {
-    const int u = ikt % kScaleGroup;
-    if (u == 0) gload = gload + 1 == L::GROUPS ? 0 : gload + 1;
-    load_scales(ikt / kScaleGroup + 1, gload, u);
-  };
-  constexpr int EARLY = PER / 2;                    // loads of a stage that are requested in its step's last two passes
-#pragma unroll 1
-  for (int s = 0; s < L::AHEAD - 1; ++s) {                     // nb >= AHEAD (kTileMinStages)
-    begin_stage();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) load(i);
-    loaded();
+    return;                                                    // nothing is in flight
   }
-  begin_stage();
-#pragma unroll
-  for (int i = 0; i < EARLY; ++i) load(i);
 
-  // ---- compute side
-  // A step multiplies a stage: a pass for each of the wave's column blocks over its row blocks.  Nothing waits
-  // for LDS: a column block is read two passes ahead, the next stage's rows in the last pass, each into the registers
-  // of the ones that it has just used; and the loads of the stages to come are spread over the passes.
-  const uint32_t aoff = (16 * wm + l16) * kBlock + 16 * (q ^ (l16 >> 1));   // piece q; piece q + 4 is 64 bytes up or down
-  uint4 fa[MI][2], fb[4][2];
+  // ---- the waves that multiply --------------------------------------------------------
+  // A step goes through the wave's blocks by quarters, each a half of its row blocks with a half of its column
+  // blocks, in an order in which neighbours share a half: rows 0 columns 0, rows 0 columns 1, rows 1 columns 1,
+  // rows 1 columns 0.  A quarter of the operands is read during each quarter, into registers whose values are used up: this
+  // step's columns 1 and rows 1, the next step's rows 0 and, each after its last use, columns 0.  (Rows all read in the
+  // step's last quarter, 80 KiB for LDS within 256 cycles of matrix instructions: FFN of 4096 tokens x 8 of 128 experts,
+  // 2048 x 768, 313 us instead of 297.  Columns alternating from step to step: two copies of the step, which spill.)
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t aoff = (16 * wm + (lane & 15)) * kBlock + 16 * ((lane >> 4) ^ ((lane & 15) >> 1));   // piece q; piece q + 4 is 64 bytes up or down
+  uint4 fa[MI][2], fb[NJ][2];
   float sx[MI], sw[2];
   int cgroup = 0;                                              // slot of the scales that are read
   uint32_t cslot = 0, st = 0;                                  // the stage that is read: ring slot, place in LDS
@@ -622,50 +644,50 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
   auto read_b = [&](int j) MOE_INLINE {
     const int b = M == kGateUp ? (j < NJ / 2 ? wn * (NJ / 2) + j : C::BN / 32 + wn * (NJ / 2) + j - NJ / 2) : wn * NJ + j;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) fb[j & 3][h] = at16(st + L::A + h * L::B + b * 1024 + lane * 16);
+    for (int h = 0; h < 2; ++h) fb[j][h] = at16(st + L::A + h * L::B + b * 1024 + lane * 16);
   };
   auto read_scales = [&]() MOE_INLINE {
     const uint32_t sc = L::SCALE0 + cgroup * L::SCALES + ckt % kScaleGroup * 4;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int blk = wm + WM * i;
-      sx[i] = at4(sc + (blk % NW) * L::WSCALES + (blk / NW) * 256 + l16 * 16);
-    }
-    const uint32_t w = sc + wave * L::WSCALES + C::ADMA * 256;
-    sw[0] = at4(w + 16 * (M == kGateUp || C::BN == kBlock ? 0 : wn * NJ * 16 / kBlock));
-    sw[1] = M == kGateUp ? at4(w + 16) : sw[0];
+    for (int i = 0; i < MI; ++i) sx[i] = at4(sc + (16 * (wm + WM * i) + (lane & 15)) * 16);
+    sw[0] = at4(sc + L::WSCALE + 16 * (M == kGateUp || C::BN == kBlock ? 0 : wn * NJ * 16 / kBlock));
+    sw[1] = M == kGateUp ? at4(sc + L::WSCALE + 16) : sw[0];
   };
-  wait_loads_barrier<(L::AHEAD - 2) * PER + EARLY>();
+  barrier();                                                   // stage 0 has arrived
   read_scales();
+  constexpr int HA = MI / 2, HB = NJ / 2, QUARTER = HA * HB;
 #pragma unroll
-  for (int i = 0; i < MI; ++i) read_a(i);
-  read_b(0);
-  read_b(1);
+  for (int i = 0; i < HA; ++i) read_a(i);
+#pragma unroll
+  for (int j = 0; j < HB; ++j) read_b(j);
 #pragma unroll 1
   for (int cr = 0; cr < n_my; ++cr) {
-    const Item it = cur;
-    const int par = cr & 1;
-    cur = nxt;
-    if (cr + 2 < n_my) nxt = item_of(cr + 2);
-    load_list(nxt, par);                                       // in place of tile cr's
+    const Item it = item_of(cr);
     f32x4 acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     // A product is scaled into acc LAG products later; the step's last ones in the next step.
-    constexpr int LAG = EXACT ? MI : 3, RING = EXACT ? 2 * MI : 4, ALL = MI * NJ;
+    constexpr int LAG = EXACT ? QUARTER : 3, RING = EXACT ? 2 * QUARTER : 4;
+    static_assert(LAG <= QUARTER && 4 * QUARTER % RING == 0, "");
     f32x4 t[RING];
     float s[2][MI], s_last[MI];                                // rows' times gate's (the only), up's; of the step before
 #pragma unroll
     for (int i = 0; i < RING; ++i) t[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < MI; ++i) s_last[i] = 0.f;
-    auto add = [&](int n) MOE_INLINE {                         // product n of this step, n < 0: of the step before
-      const int m = (n + ALL) % ALL, i = m % MI, j = m / MI;
-      const float by = n < 0 ? s_last[i] : s[M == kGateUp && j >= NJ / 2 ? 1 : 0][i];
+    // Row and column block of product n of a step's order, n < 0: of the step before.
+    auto row_of = [](int n) MOE_INLINE { return (n < 0 || n >= 2 * QUARTER ? HA : 0) + (n + 4 * QUARTER) % HA; };
+    auto col_of = [](int n) MOE_INLINE {
+      const int quarter = (n + 4 * QUARTER) / QUARTER % 4;
+      return (quarter == 1 || quarter == 2 ? HB : 0) + (n + 4 * QUARTER) % QUARTER / HA;
+    };
+    auto add = [&](int n) MOE_INLINE {
+      const int i = row_of(n), j = col_of(n);
+      const float by = n < 0 ? s_last[i] : s[M == kGateUp && j >= HB ? 1 : 0][i];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t[m % RING][r], by, acc[i][j][r]);
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t[(n + 4 * QUARTER) % RING][r], by, acc[i][j][r]);
     };
 #pragma unroll 1
     for (int kt = 0; kt < nb; ++kt) {
@@ -674,68 +696,52 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
         s[0][i] = sx[i] * sw[0];
         s[1][i] = sx[i] * sw[1];
       }
-      Wide x[EXACT ? MI : 1];
-      if constexpr (EXACT) {
+      Wide x[EXACT ? HA : 1], w[EXACT ? HB : 1];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) x[i] = widen(fa[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if (j == NJ - 2) {
-          // the next stage is complete in LDS, and every wave has read all of this one
-          wait_loads_reads_barrier<(L::AHEAD - 2) * PER>();
-          cslot = cslot + 1 == L::STAGES ? 0 : cslot + 1;
+      for (int quarter = 0; quarter < 4; ++quarter) {
+        const int i0 = quarter < 2 ? 0 : HA, j0 = quarter == 1 || quarter == 2 ? HB : 0;
+        if (quarter == 2) {
+          lds_barrier();                                       // barrier of this step: this wave has read its stage
+          cslot = cslot + 1 == STAGES ? 0 : cslot + 1;
           ckt = ckt + 1 == nb ? 0 : ckt + 1;
           st = cslot * L::STAGE;
           if (ckt % kScaleGroup == 0) cgroup = cgroup + 1 == L::GROUPS ? 0 : cgroup + 1;
-          // The sums so far are made here: the compiler would move them behind the branches to come, and keep all
-          // products.  It counts these empty statements as wait states between a matrix instruction and the use of
-          // its result, so real ones follow (11 are needed).
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int m = 0; m < NJ; ++m) asm volatile("" : "+v"(acc[i][m]));
-          asm volatile("s_nop 10");
-          if (ikt == nb) {                                     // go on with the next tile's stages
-            aim(cur, par ^ 1);
-            ikt = 0;
-#pragma unroll
-            for (int u = 0; u <= C::ADMA; ++u) load_scales(0, gload, u);   // the slot after its predecessor's last group
-          }
-          begin_stage();
-          read_scales();
         }
-        read_b((j + 2) % NJ);
         if constexpr (EXACT) {
-          const Wide w = widen(fb[j & 3]);
+          if (quarter % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < HA; ++i) x[i] = widen(fa[i0 + i]);
+          }
+          if (quarter != 2) {
+#pragma unroll
+            for (int j = 0; j < HB; ++j) w[j] = widen(fb[j0 + j]);
+          }
 #pragma unroll
           for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-              f32x4& to = t[(j * MI + i) % RING];
-              to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x[EXACT ? i : 0].v[h], h ? to : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            for (int n = 0; n < QUARTER; ++n) {
+              f32x4& to = t[(quarter * QUARTER + n) % RING];
+              to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[EXACT ? n / HA : 0].v[h], x[EXACT ? n % HA : 0].v[h],
+                                                           h ? to : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
             }
         }
+        // What is read now is used in the next quarter first (rows 0 in the one after).
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          if constexpr (!EXACT) t[(j * MI + i) % RING] = mfma_codes(fb[j & 3], fa[i]);
-          if (j == NJ - 1) read_a(i);
-          add(j * MI + i - LAG);
-        }
-        constexpr int OTHERS = NJ / 4;
-        // a stage's loads: the first EARLY in the last two passes, the others in all but the last three
-        if (j >= NJ - 2) {
-#pragma unroll
-          for (int l = (j - (NJ - 2)) * EARLY / 2; l < (j - (NJ - 3)) * EARLY / 2; ++l) load(l);
-        } else if (j < OTHERS) {
-#pragma unroll
-          for (int l = EARLY + j * (PER - EARLY) / OTHERS; l < EARLY + (j + 1) * (PER - EARLY) / OTHERS; ++l) load(l);
-          if (j == OTHERS - 1) loaded();
+        for (int n = 0; n < QUARTER; ++n) {
+          const int m = quarter * QUARTER + n;
+          if constexpr (!EXACT) t[m % RING] = mfma_codes(fb[j0 + n / HA], fa[i0 + n % HA]);
+          const int u = n / HA;                                // a read per operand
+          if (quarter == 0 && n % HA == 0) read_b(HB + u);
+          if (quarter == 1 && n < HA) read_a(HA + n);
+          if (quarter == 2 && n < HA) read_a(n);
+          if (quarter == 3 && n % HA == HA - 1) read_b(u);
+          if (quarter == 2 && n == QUARTER - 1) read_scales();
+          add(m - LAG);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = 0; i < MI; ++i) s_last[i] = s[M == kGateUp ? 1 : 0][i];
+      for (int i = HA; i < MI; ++i) s_last[i] = s[0][i];
     }
 #pragma unroll
     for (int n = -LAG; n < 0; ++n) add(n);
@@ -777,17 +783,11 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
         const int row = it.row(min(m, it.rows - 1));
         uint8_t* orow = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * cols;
         if (m < it.rows && wn == 0 && q == 0) p.out_scale[static_cast<size_t>(it.chunk) * p.n_rows + row] = qs.base;
-        if constexpr (NJ / 2 == 4) {
-          transpose_rows(d);                                   // now lane 16 q + r: the 16 columns of block q
-          const int n = n0 + 16 * (wn * 4 + q);
-          if (m < it.rows && n < cols) *reinterpret_cast<uint4*>(orow + n) = make_uint4(d[0], d[1], d[2], d[3]);
-        } else {
-          static_assert(NJ / 2 == 2, "one store per row and lane");
-          swap32(d[0], d[1]);                                  // row q = 2 a + b gets columns 8 b .. 8 b + 7 of block a
-          swap16(d[0], d[1]);
-          const int n = n0 + 16 * (wn * 2 + (q >> 1)) + 8 * (q & 1);
-          if (m < it.rows && n < cols) *reinterpret_cast<uint2*>(orow + n) = make_uint2(d[0], d[1]);
-        }
+        static_assert(NJ / 2 == 2, "one store per row and lane");
+        swap32(d[0], d[1]);                                  // row q = 2 a + b gets columns 8 b .. 8 b + 7 of block a
+        swap16(d[0], d[1]);
+        const int n = n0 + 16 * (wn * 2 + (q >> 1)) + 8 * (q & 1);
+        if (m < it.rows && n < cols) *reinterpret_cast<uint2*>(orow + n) = make_uint2(d[0], d[1]);
       }
     } else {
 #pragma unroll
@@ -820,8 +820,6 @@ __global__ __launch_bounds__(C::NT, C::NW / 4) void tile_fp8(ProductArgs p) {
       }
     }
   }
-  // the stages requested past the last tile land in LDS: not after this block has left it
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <class Tile, Mode M, bool EXACT, class Out>
@@ -855,8 +853,7 @@ void launch_many(const ProductArgs& p, hipStream_t stream) {
   } else if constexpr (exact) {
     launch_tile<TileExact, M, true, Out>(p, stream);
   } else {
-    if (plan.kernel == Kernel::kTileWide) launch_tile<TileWide, M, false, Out>(p, stream);
-    else launch_tile<TileLow, M, false, Out>(p, stream);
+    launch_tile<TileCodes, M, false, Out>(p, stream);
   }
 }
 

@@ -19,46 +19,43 @@ constexpr int kBlock = 128;          // columns that share a scale, and K of a s
 constexpr int kHalf = 64;            // columns of a packed block
 
 // ---- tile_fp8's tiles and their LDS ---------------------------------------------------
-// MI x NJ blocks of 16x16 per wave, WM x WN waves.
-template <int MI_, int NJ_, int WM_, int WN_>
+// MI x NJ blocks of 16x16 per wave that multiplies, WM x WN of them, and waves that only load.
+constexpr int kLoaders = 4;
+template <int MI_, int NJ_, int WM_, int WN_, int STAGES_>
 struct TileCfg {
-  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = i8::kLanes * NW;
-  static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN;
-  static constexpr int ADMA = BM / 16 / NW, BDMA = BN / 16 / NW;   // a wave's 16-row blocks
-  static_assert(ADMA >= 1 && ADMA < 4 && BDMA >= 1, "a load of scales per stage: each 16 rows', the matrix's");
+  static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, NW = WM * WN, NT = i8::kLanes * (NW + kLoaders);
+  static constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN, STAGES = STAGES_;
+  static constexpr int AL = BM / 8 / kLoaders;                 // DMA instructions of a stage per loader: of rows (8 each),
+  static constexpr int BL = BN / 16 / kLoaders;                // of weights, 16-row blocks (two halves each)
+  static constexpr int SL = BM / 16 / kLoaders;                // of scales, 16 rows each, for a group of stages
+  static_assert(SL >= 1 && SL < 3 && BL >= 1, "a load of scales per stage, but the group's first: rows', the matrix's");
 };
-using TileWide = TileCfg<4, 8, 4, 2>;    // 256 rows x 256 weight rows
-using TileLow = TileCfg<4, 4, 2, 4>;     // 128 rows x 256
-using TileExact = TileCfg<4, 4, 4, 2>;   // 256 rows x 128
+using TileCodes = TileCfg<4, 4, 2, 4, 3>;   // 128 rows x 256 weight rows
+using TileExact = TileCfg<4, 4, 2, 2, 4>;   // 128 rows x 128
 
-constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile (TileLds)
+constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile: a row list arrives within them (tile_fp8)
 constexpr int kScaleGroup = 4;           // stages whose scales are loaded together
 template <class C, Mode M>
 struct TileLds {
   static constexpr int A = C::BM * kBlock, B = C::BN * kHalf;  // bytes of a stage's rows, of half a stage's weights
   static constexpr int STAGE = A + 2 * B;
-  // scales of a group of stages: a wave's are its rows' (16 bytes each), then those of two blocks of the matrix
-  static constexpr int WSCALES = (16 * C::ADMA + 2) * 4 * kScaleGroup, SCALES = C::NW * WSCALES, GROUPS = 3;
-  static constexpr int WROWS = 16 * C::ADMA * 4, ROWS = C::NW * WROWS;
-  static constexpr int FIXED = GROUPS * SCALES + 2 * ROWS + (M == kGateUp ? C::WN * C::BM * 4 : 0) + 16;
-  static constexpr int plan_bytes(int G) { return 4 * C::NW + 8 * (G + 1); }
-  static constexpr int kMostGroups = 2 * 512 + 256;
-  static constexpr int STAGES = (i8::kLdsPerCu - FIXED - plan_bytes(kMostGroups)) / STAGE;
-  static constexpr int AHEAD = STAGES;                         // stages requested before the first is multiplied
-  static_assert(STAGES >= 2 && (M != kGateUp || C::BN == 2 * kBlock), "a kGateUp tile holds the columns of one scale");
-  static constexpr int RING = STAGES * STAGE, PLAN_ = RING + FIXED;
-  static constexpr int SCALE0 = RING;                          // scales of three groups of stages
-  static constexpr int LIST = RING + GROUPS * SCALES;                            // row list of two tiles
-  static constexpr int MAX = LIST + 2 * ROWS;                  // kGateUp: largest magnitudes
-  static constexpr int ZERO = PLAN_ - 16;                      // zeros
-  static constexpr int PLAN = PLAN_;                    // sums over waves, tiles before each group, group offsets
-  static int bytes(int G) { return PLAN + plan_bytes(G); }
-  // The stages requested before a block's first product are all its first tile's: what follows is
-  // the next tile's, whose sources are set when the first tile starts.
-  static_assert(AHEAD <= kTileMinStages, "a tile has more stages than are requested ahead");
+  static constexpr int WSCALE = C::BM * 4 * kScaleGroup;       // in a group of scales: the rows' (16 bytes each), then of two
+  static constexpr int SCALES = WSCALE + 2 * 4 * kScaleGroup;  // blocks of the matrix
+  static constexpr int GROUPS = C::STAGES;                     // (tile_fp8)
+  static_assert(M != kGateUp || C::BN == 2 * kBlock, "a kGateUp tile holds the columns of one scale");
+  static_assert(C::STAGES - 1 <= kTileMinStages, "a tile's row list arrives before its first stage is requested");
+  static constexpr int SCALE0 = C::STAGES * STAGE;
+  static constexpr int LIST = SCALE0 + GROUPS * SCALES;        // row lists of two tiles
+  static constexpr int MAX = LIST + 2 * C::BM * 4;             // kGateUp: largest magnitudes
+  static constexpr int ZERO = MAX + (M == kGateUp ? C::WN * C::BM * 4 : 0);
+  static constexpr int PLAN = ZERO + 16;                       // sums over waves, tiles before each group, group offsets
+  static constexpr int bytes(int G) { return PLAN + 4 * (C::NW + kLoaders) + 8 * (G + 1); }
 };
+constexpr int kTileMostGroups = 800;     // whose lists fit beside the stages
+static_assert(TileLds<TileCodes, kGateUp>::bytes(kTileMostGroups) <= i8::kLdsPerCu &&
+              TileLds<TileExact, kLinear>::bytes(kTileMostGroups) <= i8::kLdsPerCu, "a block's LDS");
 
-enum class Kernel { kFew, kStream, kTileLow, kTileWide, kTileExact };
+enum class Kernel { kFew, kStream, kTileCodes, kTileExact };
 struct Plan {
   Kernel kernel;
   int width;    // few_fp8: 16-column blocks of an item; stream_fp8: 16-row blocks of a tile
@@ -66,8 +63,20 @@ struct Plan {
 };
 inline Launch launch_of(const Plan& p) { return i8::launch_of(i8::Plan{i8::Kernel::kStream, p.width, p.blocks}); }
 
-constexpr int kTileMinAvg = 64, kWideMinAvg = 192;
-constexpr int kTileMinItems = 512;
+// Where tile_fp8 takes over from stream_fp8: few rows per group leave its tiles of 128 empty, and a small output
+// leaves CUs without one, each of them as long as K.  us, stream_fp8 / tile_fp8 (products alone of 2^20 outputs, FFNs of groups):
+//   outputs  linear 2048 -> 2048, 1024 rows (2.0) 20.9 / 22.5, 1536 rows (3.0) 28.8 / 23.4; 1024 -> 512, 2048 rows (1.0)
+//            13.5 / 15.5, 3000 rows (1.5) 18.7 / 15.8; 2560 -> 2560, 512 rows (1.3) 22.3 / 25.5, 768 rows (1.9) 31.2 / 26.2;
+//            fp32 out: 2048 -> 2048, 1536 rows 28.7 / 25.6; 1024 -> 512, 2048 rows 13.5 / 16.0
+//   rows     FFN of 64 groups, 2048 x 1024, 32 rows each 98 / 102, 48 rows 111 / 106, 64 rows 125 / 108; of 128 groups, 2880 x
+//            2880, 24 rows 577 / 615, 48 rows 790 / 632; fp32 out: 64 groups 2048 -> 1024, 32 rows 36.5 / 44.1, 64 rows 46.0 / 46.6
+constexpr int kTileMinAvg = 40, kTileMinAvgExact = 64;
+constexpr long long kTileMinOutputs = 7 << 18;
+
+// Rows of stream_fp8's tiles, 16 * mf: 16 only where that leaves no CU a second item.  us with 16 / 32 rows: linear
+// 2048 -> 2048, 256 rows (256 items of 16) 9.4 / 12.0, 300 rows 13.4 / 12.2; FFN of 8 groups of 16 rows, 1472 x 832,
+// 18.7 / 21.3, of 128 groups of 8 rows, 2880 x 2880, 582 / 547, of 16 rows 637 / 559.
+constexpr int kSmallItems = 256;
 
 // The FFN's products of few rows (both of them: the SwiGLU product is kept in fp32 then).
 inline bool few_ffn(int n_rows, int I) { return i8::few(n_rows, I); }
@@ -83,9 +92,10 @@ inline Plan few_plan(Mode m, const Sizes& s) {
 inline Plan many_plan(Mode m, bool exact, const Sizes& s) {
   const int avg = s.n_rows / s.sequences();
   const long long area = static_cast<long long>(s.n_rows) * s.cols;
-  if (avg > kTileMinAvg && area >= kTileMinItems * 64ll * 128 && s.K > (kTileMinStages - 1) * kBlock)
-    return Plan{exact ? Kernel::kTileExact : avg >= kWideMinAvg ? Kernel::kTileWide : Kernel::kTileLow, 0, 0};
-  const int nch = (s.cols + kBlock - 1) / kBlock, mf = i8::pick_mf(avg);
+  if (avg >= (exact ? kTileMinAvgExact : kTileMinAvg) && area >= kTileMinOutputs && s.K > (kTileMinStages - 1) * kBlock &&
+      s.groups() <= kTileMostGroups)
+    return Plan{exact ? Kernel::kTileExact : Kernel::kTileCodes, 0, 0};
+  const int nch = (s.cols + kBlock - 1) / kBlock, mf = max_m_tiles(s, 16) * nch <= kSmallItems ? 1 : 2;
   return Plan{Kernel::kStream, mf, item_grid(max_m_tiles(s, 16 * mf), nch)};
 }
 

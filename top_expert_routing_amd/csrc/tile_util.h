@@ -137,11 +137,11 @@ template <int N>
 __device__ __forceinline__ void wait_loads_barrier() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(N) : "memory");
 }
-// The same, and the wave's LDS reads are done: what all waves have read may be overwritten.
 template <int N>
-__device__ __forceinline__ void wait_loads_reads_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" : : : "memory"); }
 // LDS writes of all waves before LDS reads of all waves, DMA loads left in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 
