@@ -32,6 +32,7 @@ sys.path.insert(0, ROOT)
 PEAK_HBM_GBS = 8000.0          # MI355X HBM3E
 PEAK_BF16_TFLOPS = 2500.0      # MI355X dense bf16 MFMA
 PEAK_I8_TOPS = 5000.0          # MI355X dense int8 MFMA
+PEAK_FP8_TFLOPS = 5000.0       # MI355X dense fp8 MFMA
 PEAK_F32_TFLOPS = 157.3        # MI355X fp32 vector
 METRIC = "MoE-layer tokens/s; decode HBM GB/s and prefill MFMA util vs MI355X peak"
 FFN_SOURCE = os.path.join(ROOT, "top_expert_routing_amd", "csrc", "ffn.hip")
@@ -58,6 +59,13 @@ def parse():
     ap.add_argument("--int8-weights", action="store_true",
                     help="expert weights as int8 codes with per-channel scales and int8 activations "
                          "(moe_grouped_ffn_i8); the CPU baseline leg is skipped in this mode")
+    ap.add_argument("--fp8-block-weights", action="store_true",
+                    help="expert weights as E4M3 codes with a scale per 128 x 128 block and E4M3 activations with one "
+                         "per 128 columns (moe_grouped_ffn_fp8); the CPU baseline leg is skipped in this mode")
+    ap.add_argument("--norm", action="store_true",
+                    help="start the step with the RMS norm of the tokens plus an fp32 residual, which it updates "
+                         "(moe_rmsnorm; with --fp8-block-weights it writes the experts' codes); the router and the "
+                         "experts read the normalised rows; the CPU baseline leg is skipped in this mode")
     ap.add_argument("--unpacked-weights", action="store_true",
                     help="keep the [E+S][rows][K] weight layout (moe_grouped_ffn) on bf16 workloads; by "
                          "default their weights are pre-packed once before timing (pack_weights) and the FFN "
@@ -365,16 +373,26 @@ def main():
         print("--int8-weights needs a bf16 workload with d and I multiples of 64 and goes with no other weight option",
               file=sys.stderr)
         sys.exit(2)
+    block = bool(args.fp8_block_weights)
+    if block and (s.dtype != "bf16" or fp8 or int8 or args.fused_combine or args.unpacked_weights or s.d % 64 or s.I % 64):
+        print("--fp8-block-weights needs a bf16 workload with d and I multiples of 64 and goes with no other weight option",
+              file=sys.stderr)
+        sys.exit(2)
     # bf16 batches run on pre-packed weights unless asked otherwise
-    packable = not fp8 and not int8 and s.dtype == "bf16" and s.d % 32 == 0 and s.I % 32 == 0
+    packable = not fp8 and not int8 and not block and s.dtype == "bf16" and s.d % 32 == 0 and s.I % 32 == 0
     packed = packable and not args.unpacked_weights
     # FP8 codes are packed too when d and I are multiples of 64
     fp8_packed = fp8 and s.d % 64 == 0 and s.I % 64 == 0 and not args.unpacked_weights
-    # expert weight bytes (fp8, int8: codes plus one fp32 scale per weight row)
-    expert_bytes = 3 * s.d * s.I + (2 * s.I + s.d) * 4 if fp8 or int8 else 3 * s.d * s.I * esize
+    # expert weight bytes (fp8, int8: codes plus one fp32 scale per weight row, or per 128 x 128 block)
+    expert_bytes = 3 * s.d * s.I + (2 * s.I + s.d) * 4 if fp8 or int8 else \
+        3 * (s.d * s.I + 4 * -(-s.d // 128) * -(-s.I // 128)) if block else 3 * s.d * s.I * esize
     all_w = (s.E + s.S) * expert_bytes
     copies = args.weight_copies or max(1, int(np.ceil(3 * 2**30 / all_w)))
-    if int8:
+    if block:
+        q = [moe.quantize_fp8_blocks(w) for w in (wl.w_gate, wl.w_up, wl.w_down)]
+        base = tuple(t for c, sc in q for t in (moe.pack_fp8_codes(c), sc))
+        wsets = [base] + [tuple(t.clone() for t in base) for _ in range(copies - 1)]
+    elif int8:
         q = [moe.quantize_rows_i8(w) for w in (wl.w_gate, wl.w_up, wl.w_down)]
         base = tuple(t for c, sc in q for t in (moe.pack_i8_codes(c), sc))
         wsets = [base] + [tuple(t.clone() for t in base) for _ in range(copies - 1)]
@@ -399,30 +417,38 @@ def main():
     if args.router:
         g = torch.Generator().manual_seed(1234)
         w_router = (torch.randn((s.E, s.d), generator=g) * 0.02).to(wl.torch_dtype).to(dev)
-    w16 = (wl.w_gate, wl.w_up, wl.w_down) if fp8 or int8 else wsets[0]     # the layer's bf16 / fp32 weights
+    norm = residual = None
+    if args.norm:
+        g = torch.Generator().manual_seed(4321)
+        norm = ((1 + 0.1 * torch.randn(s.d, generator=g)).to(wl.torch_dtype).to(dev), 1e-6)
+        residual = torch.randn((s.T, s.d), generator=g).to(dev)
+    w16 = (wl.w_gate, wl.w_up, wl.w_down) if fp8 or int8 or block else wsets[0]     # the layer's bf16 / fp32 weights
     layer = moe.MoeLayer(s.E, s.k, s.d, s.I, s.T, wl.torch_dtype, *w16, packed_weights=packed or fp8_packed,
                          n_shared=s.S, n_priority=s.n_priority, renormalize=bool(s.renormalize),
                          stats_layers=s.stats_layers, req_offsets=wl.req_offsets, device=dev,
                          topk_ids=stats_ids[0], w_router=w_router, fp8_weights=wsets[0] if fp8 else None,
-                         fused_combine=args.fused_combine, int8_weights=wsets[0] if int8 else None)
+                         fused_combine=args.fused_combine, int8_weights=wsets[0] if int8 else None,
+                         fp8_block_weights=wsets[0] if block else None, norm=norm)
     for l in range(1, s.stats_layers):      # the other layers' ids, produced before timing
         moe.gate(wl.stats_logits[l].contiguous(), s.k, True, stats_ids[l],
                  torch.empty((s.T, s.k), device=dev))
-    # One stream, in path order: (router,) gate, statistics (they need only the gate's
+    # One stream, in path order: (norm, router,) gate, statistics (they need only the gate's
     # ids), permute, FFN, combine.  (A second stream for the statistics costs
     # two cross-queue waits per step, more than the statistics themselves.)
     stream = torch.cuda.Stream(dev)
     call_sets = []
     for ws in wsets:
-        if int8:
+        if block:
+            layer.fp8_block_weights = ws
+        elif int8:
             layer.int8_weights = ws
         elif fp8:
             layer.fp8_weights = ws
         else:
             layer.w_gate, layer.w_up, layer.w_down = ws
-        call_sets.append(layer.bound_calls(wl.logits, wl.x, stats_ids, stream.cuda_stream))
+        call_sets.append(layer.bound_calls(wl.logits, wl.x, stats_ids, stream.cuda_stream, residual=residual))
     names = [c[0] for c in call_sets[0]]
-    first = [names.index(n) for n in ("moe_router", "moe_gate", "moe_stats") if n in names]
+    first = [names.index(n) for n in ("moe_rmsnorm", "moe_router", "moe_gate", "moe_stats") if n in names]
     order = first + [j for j in range(len(names)) if j not in first]
 
     def step(i, ev=None):
@@ -491,7 +517,7 @@ def main():
         for i in range(K):
             step(i, evs[i])
     torch.cuda.synchronize()
-    diag = 0 if int8 else int(layer.ffn_ws[-4:].view(torch.int32).item())   # the int8 call has no waits
+    diag = 0 if int8 or block else int(layer.ffn_ws[-4:].view(torch.int32).item())   # those calls have no waits
     if diag != 0:
         raise RuntimeError("the FFN's diagnostic word is set: a wait of the persistent tile queue gave up")
     per_call = {n: 0.0 for n in names}
@@ -505,12 +531,13 @@ def main():
     N = s.N
     ffn_bytes = used_experts * expert_bytes + 2 * N * s.d * esize
     ffn_flops = 2.0 * N * 3 * s.d * s.I
-    ffn_name = "moe_grouped_ffn_i8" if int8 else \
+    ffn_name = "moe_grouped_ffn_fp8" if block else "moe_grouped_ffn_i8" if int8 else \
         ("moe_grouped_ffn_fp8w_packed" if fp8_packed else "moe_grouped_ffn_fp8w") if fp8 else \
         "moe_grouped_ffn_combine" if args.fused_combine else \
         "moe_grouped_ffn_packed" if packed else "moe_grouped_ffn"
     ffn_s = per_call[ffn_name] * 1e-3
-    peak_flops = PEAK_F32_TFLOPS if s.dtype == "f32" else PEAK_I8_TOPS if int8 else PEAK_BF16_TFLOPS
+    peak_flops = PEAK_F32_TFLOPS if s.dtype == "f32" else PEAK_I8_TOPS if int8 else \
+        PEAK_FP8_TFLOPS if block else PEAK_BF16_TFLOPS
     intensity = ffn_flops / ffn_bytes
     ridge = peak_flops * 1e12 / (PEAK_HBM_GBS * 1e9)
     if intensity < ridge:
@@ -522,13 +549,13 @@ def main():
         roof = {"bound": "mfma", "achieved": round(achieved, 1), "peak": peak_flops, "unit": "TFLOP/s",
                 "frac": round(achieved / peak_flops, 4)}
     # the committed counters are for the default mode of each workload
-    traffic = None if fp8 or int8 or args.unpacked_weights or args.fused_combine else traffic_for(args.workload)
+    traffic = None if fp8 or int8 or block or args.norm or args.unpacked_weights or args.fused_combine else traffic_for(args.workload)
     roof["traffic"] = None if traffic is None else round(traffic)
     # the library's path choice for batches with a priority segment: bf16
     # prefill-sized groups, or packed FP8 codes on 128-row GEMM tiles
     avg = s.N // s.G
     queue = (s.n_priority > 0 and os.environ.get("LIBMOE_FFN_QUEUE", "1") != "0" and
-             ((not fp8 and not int8 and s.dtype == "bf16" and s.d % 32 == 0 and s.I % 32 == 0 and avg > 48) or
+             ((not fp8 and not int8 and not block and s.dtype == "bf16" and s.d % 32 == 0 and s.I % 32 == 0 and avg > 48) or
               (fp8_packed and s.d >= 128 and s.I >= 128 and 48 < avg < 256)))
     roof["kernel"] = (f"{ffn_name} (" + ("one persistent launch: decode-priority tile queues" if queue else
                                          "gate/up launch + down launch with the combine in its epilogue + "
@@ -562,9 +589,10 @@ def main():
         "scaling": "weak", "vs_baseline": None, "dtype": s.dtype, "data": "synthetic",
         "config": {"workload": args.workload, "T": s.T, "E": s.E, "k": s.k, "n_shared": s.S, "d": s.d,
                    "I": s.I, "n_priority": s.n_priority, "stats_layers": s.stats_layers,
-                   "weight_copies": copies, "union": union, "router": bool(args.router),
+                   "weight_copies": copies, "union": union, "router": bool(args.router), "norm": bool(args.norm),
                    "expert_weights": ("fp8_e4m3 + fp32 row scales" + (", packed 16x64 blocks" if fp8_packed else ""))
                    if fp8 else "int8 + fp32 channel scales, packed 16x64 blocks" if int8 else
+                   "fp8_e4m3 + fp32 scales of 128x128 blocks, packed 16x64 blocks" if block else
                    f"{s.dtype}, packed 16x32 blocks" if packed else s.dtype},
         "roofline": roof,
         "per_call_us": {n: round(v * 1e3, 2) for n, v in per_call.items()},
@@ -575,7 +603,7 @@ def main():
         out["signature_recording"] = signature
     if dseg is not None:
         out["decode_segment"] = dseg
-    if not args.no_cpu_baseline and not fp8 and not int8:
+    if not args.no_cpu_baseline and not fp8 and not int8 and not block and not args.norm:
         out["cpu_baseline"] = cpu_baseline(wl, args.cpu_seconds, w_router)
     line = json.dumps(out)
     print(line, flush=True)

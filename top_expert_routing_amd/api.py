@@ -997,13 +997,16 @@ class MoeLayer:
     routing layer's own ids are written into stats_ids[0] by the gate).  With
     `w_router` ([E][d], the input dtype) the router projection runs first and
     the gate reads its logits; `forward` then ignores the logits argument.
+    With `norm` ((weight [d], eps)) the layer starts with the RMS norm of its
+    input, to which `forward` and `bound_calls` then add a residual, if given one,
+    in place; the router and the experts read the normalised rows.
     Nothing is allocated per call.
     """
 
     def __init__(self, E, k, d, I, T, dtype, w_gate, w_up, w_down, n_shared=0, n_priority=0,
                  renormalize=True, stats_layers=0, req_offsets=None, device="cuda", topk_ids=None,
                  fused_gather=True, w_router=None, fp8_weights=None, packed_weights=False, fused_combine=False,
-                 int8_weights=None, routing=None):
+                 int8_weights=None, routing=None, fp8_block_weights=None, norm=None):
         dev = torch.device(device)
         # fp8_weights = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down):
         # the FFN runs moe_grouped_ffn_fp8w on them instead of w_gate / w_up / w_down
@@ -1022,6 +1025,15 @@ class MoeLayer:
         self.int8_weights = int8_weights
         if int8_weights is not None and (fp8_weights is not None or self.fused_combine or dtype != torch.bfloat16):
             raise ValueError("int8_weights serve bf16 tokens, without fp8_weights or fused_combine")
+        # fp8_block_weights = (codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down) of
+        # quantize_fp8_blocks, codes from pack_fp8_codes: the FFN runs moe_grouped_ffn_fp8 on E4M3 codes of the
+        # tokens, which the norm makes, or moe_quantize_blocks_fp8 without one
+        self.fp8_block_weights = fp8_block_weights
+        if fp8_block_weights is not None and (fp8_weights is not None or int8_weights is not None or self.fused_combine or
+                                              not fused_gather or dtype != torch.bfloat16):
+            raise ValueError("fp8_block_weights serve bf16 tokens read through the row list (fused_gather), without "
+                             "fp8_weights, int8_weights or fused_combine")
+        self.norm = None if norm is None else tuple(norm)
         # routing: None (moe_gate), or a dict of route()'s score, bias, n_groups, top_groups, group_rank, scale:
         # the layer's gate is moe_route
         self.routing = None if routing is None else dict(routing)
@@ -1036,6 +1048,16 @@ class MoeLayer:
             _out(self.routing["bias"], "bias", torch.float32, (E,))
         if int8_weights is not None:
             _need_i8_weights(int8_weights[0], E + n_shared, d, I, int8_weights)
+        if fp8_block_weights is not None:
+            _need_fp8_weights(fp8_block_weights[0], E + n_shared, d, I, fp8_block_weights)
+        self.xn = self.xq = self.xs = None
+        if self.norm is not None:
+            self._need_norm(d)
+            if fp8_block_weights is None or w_router is not None:
+                self.xn = torch.empty((T, d), dtype=dtype, device=dev)
+        if fp8_block_weights is not None:
+            self.xq = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev)
+            self.xs = torch.empty((T, _blocks(d)), dtype=torch.float32, device=dev)
         self.w_router = w_router
         self.logits = torch.empty((T, E), dtype=torch.float32, device=dev) if w_router is not None else None
         self.E, self.k, self.d, self.I, self.T = E, k, d, I, T
@@ -1066,6 +1088,8 @@ class MoeLayer:
             ws_bytes = ffn_combine_workspace_bytes(N, E, n_shared, self.nseg, d, I, T, k, self.packed)
         elif int8_weights is not None:
             ws_bytes = ffn_i8_workspace_bytes(N, T if fused_gather else 0, d, I, E, n_shared, self.nseg)
+        elif fp8_block_weights is not None:
+            ws_bytes = ffn_fp8_workspace_bytes(N, I, E, n_shared, self.nseg, d)
         elif fp8_weights is not None:
             ws_bytes = ffn_fp8w_workspace_bytes(N, I, E, n_shared, self.nseg, d, self.packed)
         else:
@@ -1079,6 +1103,25 @@ class MoeLayer:
             self.stats_out = {}
             self.stats_ws = torch.empty(max(stats_workspace_bytes(stats_layers, T, k, E, R), 256),
                                         dtype=torch.uint8, device=dev)
+
+    def _need_norm(self, d):
+        weight, eps = self.norm
+        if weight.dtype not in _TYPES or not eps > 0:
+            raise ValueError("norm is a bf16 or fp32 weight and a positive eps")
+        _out(weight, "the norm's weight", weight.dtype, (d,))
+
+    def prepare(self, x, residual=None):
+        """The rows that the router and the experts read: the norm's, if there is one, and the experts' FP8 codes."""
+        if self.norm is not None:
+            rmsnorm(x, self.norm[0], self.norm[1], residual=residual, y=self.xn, want_y=self.xn is not None,
+                    codes=None if self.xq is None else "fp8", q=self.xq, s=self.xs)
+            return x if self.xn is None else self.xn
+        if residual is not None:
+            raise ValueError("a residual goes with a norm")
+        if self.xq is not None:
+            _out(x, "x", torch.bfloat16, (self.T, self.d))
+            quantize_blocks_fp8(x, self.xq, self.xs)
+        return x
 
     def route(self, x):
         return router(x, self.w_router, self.logits)
@@ -1101,6 +1144,10 @@ class MoeLayer:
                                    packed=self.packed)
 
     def ffn(self, x):
+        if self.fp8_block_weights is not None:
+            return grouped_ffn_fp8(self.xq, self.xs, self.perm["group_offsets"], self.E, self.S, self.nseg,
+                                   *self.fp8_block_weights, h_sorted=self.h_sorted, workspace=self.ffn_ws,
+                                   x_rows=self.perm["sorted_token"])
         if self.int8_weights is not None:
             src = x if self.fused_gather else self.perm["x_sorted"]
             return grouped_ffn_i8(src, self.perm["group_offsets"], self.E, self.S, self.nseg, *self.int8_weights,
@@ -1129,13 +1176,14 @@ class MoeLayer:
     def stats(self, stats_ids):
         return stats(stats_ids, self.E, self.req_offsets, out=self.stats_out, workspace=self.stats_ws)
 
-    def bound_calls(self, logits, x, stats_ids=None, stream=None, stats_stream=None):
+    def bound_calls(self, logits, x, stats_ids=None, stream=None, stats_stream=None, residual=None):
         """Pre-marshalled raw C calls for one forward over fixed buffers.
 
         Returns a list of (name, fn, args) whose arguments are plain integers,
         so a timing loop pays only the ctypes call per step.  Each entry is one
-        of the libmoe calls, in path order (the router first when the layer has
-        router weights; the gate then reads the router's logits).  `stats_stream` (a raw stream
+        of the libmoe calls, in path order (the norm first when the layer has one, then
+        the router when it has router weights; the gate then reads the router's
+        logits).  `stats_stream` (a raw stream
         handle) puts the statistics call on its own stream; the caller orders it
         after the gate.
         """
@@ -1148,6 +1196,11 @@ class MoeLayer:
         n_perm = ctypes.c_size_t(self.perm_ws.numel())
         n_ffn = ctypes.c_size_t(self.ffn_ws.numel())
         calls = []
+        prepare = self._prepare_call(lib, x, residual, st)
+        if self.norm is not None:
+            calls.append(prepare)
+            x = x if self.xn is None else self.xn
+            dt = _dtype_code(self.h_sorted)
         if self.w_router is not None:
             logits = self.logits
             calls.append(("moe_router", lib.moe_router, (x.data_ptr(), self.w_router.data_ptr(), T, self.d, E, dt,
@@ -1163,6 +1216,8 @@ class MoeLayer:
                                               None if fused else self.perm["x_sorted"].data_ptr(),
                                               self.perm_ws.data_ptr(), ctypes.byref(n_perm), st)),
         ]
+        if self.norm is None and prepare is not None:
+            calls.append(prepare)
         if self.fused_combine:
             src = x.data_ptr() if fused else self.perm["x_sorted"].data_ptr()
             calls.append(("moe_grouped_ffn_combine", lib.moe_grouped_ffn_combine, (
@@ -1193,6 +1248,31 @@ class MoeLayer:
         self._keep = (n_perm, n_ffn, n_st if stats_ids is not None and self.stats_out is not None else None)
         return calls
 
+    def _prepare_call(self, lib, x, residual, st):
+        if self.norm is None and residual is not None:
+            raise ValueError("a residual goes with a norm")
+        if self.norm is None and self.xq is None:
+            return None
+        if x.dtype not in _TYPES:
+            raise TypeError("x must be bf16 or fp32")
+        _out(x, "x", torch.bfloat16 if self.norm is None else x.dtype, (self.T, self.d))
+        _same_device(self.h_sorted, x=x, residual=residual)
+        q, s = (None, None) if self.xq is None else (self.xq.data_ptr(), self.xs.data_ptr())
+        if self.norm is None:
+            return ("moe_quantize_blocks_fp8", lib.moe_quantize_blocks_fp8, (
+                x.data_ptr(), _TYPES[x.dtype], self.T, self.d, q, s, st))
+        self._need_norm(self.d)
+        weight, eps = self.norm
+        if residual is not None:
+            if residual.dtype not in _TYPES:
+                raise TypeError("the residual must be bf16 or fp32")
+            _out(residual, "residual", residual.dtype, (self.T, self.d))
+        _same_device(x, weight=weight)
+        return ("moe_rmsnorm", lib.moe_rmsnorm, (
+            x.data_ptr(), _TYPES[x.dtype], _ptr(residual), 0 if residual is None else _TYPES[residual.dtype],
+            weight.data_ptr(), _TYPES[weight.dtype], self.T, self.d, eps, _ptr(residual), _ptr(self.xn),
+            0 if self.xn is None else _TYPES[self.xn.dtype], _lib.CODES["fp8" if q else None], q, s, st))
+
     def _gate_call(self, lib, logits, st):
         if self.routing is None:
             return ("moe_gate", lib.moe_gate, (logits.data_ptr(), self.T, self.E, self.k, int(bool(self.renormalize)),
@@ -1213,6 +1293,13 @@ class MoeLayer:
         src = x.data_ptr() if fused else self.perm["x_sorted"].data_ptr()
         rows = self.perm["sorted_token"].data_ptr() if fused else None
         offs = self.perm["group_offsets"].data_ptr()
+        if self.fp8_block_weights is not None:
+            _need_fp8_weights(self.h_sorted, self.E + self.S, self.d, self.I, self.fp8_block_weights)
+            qg, sg, qu, su, qd, sd = (t.data_ptr() for t in self.fp8_block_weights)
+            return ("moe_grouped_ffn_fp8", lib.moe_grouped_ffn_fp8, (
+                self.xq.data_ptr(), self.xs.data_ptr(), rows, self.T, offs, self.N, self.E, self.S, self.nseg, self.d,
+                self.I, qg, sg, qu, su, qd, sd, self.h_sorted.data_ptr(), self.ffn_ws.data_ptr(), ctypes.byref(n_ffn),
+                st))
         if self.int8_weights is not None:
             _need_i8_weights(self.h_sorted, self.E + self.S, self.d, self.I, self.int8_weights)
             _out(x, "x", torch.bfloat16, (self.T, self.d))
@@ -1237,10 +1324,11 @@ class MoeLayer:
             self.w_up.data_ptr(), self.w_down.data_ptr(), dt, self.h_sorted.data_ptr(), self.ffn_ws.data_ptr(),
             ctypes.byref(n_ffn), st))
 
-    def forward(self, logits, x, stats_ids=None, stats_stream=None):
+    def forward(self, logits, x, stats_ids=None, stats_stream=None, residual=None):
         """Enqueue the layer on the current stream.  With `stats_stream` (a
         torch stream) the statistics run there, concurrently with the permute /
         FFN / combine chain; the current stream waits for them at the end."""
+        x = self.prepare(x, residual)
         if self.w_router is not None:
             logits = self.route(x)
         self.gate(logits)
