@@ -68,9 +68,12 @@ inline Launch launch_of(const Plan& p) { return i8::launch_of(i8::Plan{i8::Kerne
 //   outputs  linear 2048 -> 2048, 1024 rows (2.0) 20.9 / 22.5, 1536 rows (3.0) 28.8 / 23.4; 1024 -> 512, 2048 rows (1.0)
 //            13.5 / 15.5, 3000 rows (1.5) 18.7 / 15.8; 2560 -> 2560, 512 rows (1.3) 22.3 / 25.5, 768 rows (1.9) 31.2 / 26.2;
 //            fp32 out: 2048 -> 2048, 1536 rows 28.7 / 25.6; 1024 -> 512, 2048 rows 13.5 / 16.0
-//   rows     FFN of 64 groups, 2048 x 1024, 32 rows each 98 / 102, 48 rows 111 / 106, 64 rows 125 / 108; of 128 groups, 2880 x
-//            2880, 24 rows 577 / 615, 48 rows 790 / 632; fp32 out: 64 groups 2048 -> 1024, 32 rows 36.5 / 44.1, 64 rows 46.0 / 46.6
-constexpr int kTileMinAvg = 40, kTileMinAvgExact = 64;
+//   rows     where every group's one tile makes kTileManyItems (three a CU), fewer rows are enough: groups' sizes even / falling
+//            as 1 / rank: FFN of 128 groups, 2880 x 2880, 24 rows 577 / 631 and 502 / 458, 28 rows 596 / 618 and 531 / 472, 34
+//            rows 684 / 631 and 598 / 508; 128 groups, 2048 x 768, 20 rows 142 / 140 and 123 / 126, 28 rows 144 / 143 and 140 /
+//            130; else: 64 groups, 2048 x 1024, 39 rows 107 / 105 and 105 / 125, 64 rows 125 / 108 and 126 / 128
+//            fp32 out: 64 groups 2048 -> 1024, 32 rows 36.5 / 44.1, 64 rows 46.0 / 46.6
+constexpr int kTileMinAvg = 48, kTileMinAvgMany = 28, kTileMinAvgExact = 64, kTileManyItems = 768;
 constexpr long long kTileMinOutputs = 7 << 18;
 
 // Rows of stream_fp8's tiles, 16 * mf: 16 only where that leaves no CU a second item.  us with 16 / 32 rows: linear
@@ -92,10 +95,12 @@ inline Plan few_plan(Mode m, const Sizes& s) {
 inline Plan many_plan(Mode m, bool exact, const Sizes& s) {
   const int avg = s.n_rows / s.sequences();
   const long long area = static_cast<long long>(s.n_rows) * s.cols;
-  if (avg >= (exact ? kTileMinAvgExact : kTileMinAvg) && area >= kTileMinOutputs && s.K > (kTileMinStages - 1) * kBlock &&
-      s.groups() <= kTileMostGroups)
+  const int tile_cols = m == kGateUp ? TileCodes::BN / 2 : TileCodes::BN;
+  const bool many = static_cast<long long>(s.sequences()) * ((s.cols + tile_cols - 1) / tile_cols) >= kTileManyItems;
+  const int least = exact ? kTileMinAvgExact : many ? kTileMinAvgMany : kTileMinAvg;
+  if (avg >= least && area >= kTileMinOutputs && s.K > (kTileMinStages - 1) * kBlock && s.groups() <= kTileMostGroups)
     return Plan{exact ? Kernel::kTileExact : Kernel::kTileCodes, 0, 0};
-  const int nch = (s.cols + kBlock - 1) / kBlock, mf = max_m_tiles(s, 16) * nch <= kSmallItems ? 1 : 2;
+  const int nch = (s.cols + kBlock - 1) / kBlock, mf = static_cast<long long>(max_m_tiles(s, 16)) * nch <= kSmallItems ? 1 : 2;
   return Plan{Kernel::kStream, mf, item_grid(max_m_tiles(s, 16 * mf), nch)};
 }
 
