@@ -86,3 +86,21 @@ def test_ffn_against_plain_torch():
             want += wide(wd[e], sd[e])[:, b:b + 128] @ ((a[b:b + 128] / s).float().to(torch.float8_e4m3fn).double() * s)
         assert np.all(np.abs(h[n] - want.numpy()) <= err[n] + slack[n])
     assert np.median(err + slack) < 0.05 * np.median(np.abs(h))
+
+
+def test_cut_bounds_products_cut_one_by_one():
+    """Products of each eight columns cut toward zero to a multiple of 2^(E - 13), E the exponent sum of the largest
+    product's factors: the sums lose no more than cut() allows, and something."""
+    g = torch.Generator().manual_seed(5)
+    rnd = lambda *s: (torch.randn(s, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).double().numpy()
+    x, w = rnd(24, 261), rnd(40, 261)
+    lost = np.zeros((24, 40))
+    for k in range(0, 261, 8):
+        p = x[:, None, k:k + 8] * w[None, :, k:k + 8]
+        e = np.floor(np.log2(np.maximum(np.abs(x[:, None, k:k + 8]), 2.0 ** -20))) + np.floor(np.log2(np.maximum(np.abs(w[None, :, k:k + 8]), 2.0 ** -20)))
+        at = np.abs(p).argmax(2)[:, :, None]
+        step = np.exp2(np.take_along_axis(e, at, 2) - 13)
+        lost += (p - np.trunc(p / step) * step).sum(2)
+    bound = Q.cut(x, w)
+    assert np.all(np.abs(lost) <= bound) and np.abs(lost).max() > 0
+    np.testing.assert_allclose(np.linalg.norm(lost) / np.linalg.norm(x @ w.T), 3e-5, rtol=0.7)

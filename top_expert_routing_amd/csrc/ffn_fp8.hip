@@ -105,7 +105,8 @@ __device__ __forceinline__ uint32_t block_codes(const float (&v)[4], float r) {
 // columns): each wave owns 16 columns (kGateUp: 16 gate rows and 16 up rows) and
 // reads their weights once; the rows' codes are staged through LDS, 512 of K at a
 // time (256 where two row blocks and two weight blocks fill the registers), double buffered,
-// and shared by the waves.
+// and shared by the waves.  Widening the codes is hidden by the weights' arrival.
+// Bound by HBM: 128 tokens x 8 of 64 experts, 2048 -> 1408, 40 us for 190 MB (4.7 TB/s; a copy runs at 4.9).
 constexpr int kThreadsS = 512;
 constexpr int kWavesS = kThreadsS / kWave;
 
@@ -266,6 +267,8 @@ __global__ __launch_bounds__(kThreadsS, 4) void stream_fp8(ProductArgs p) {
 // A block does not hold the columns that share a scale of the SwiGLU product, so kGateUp writes
 // that in fp32 (N * I * 4 bytes, at most 80 KiB here), and kDown's waves, each on whole blocks
 // of 128 columns, quantise it as they read it.
+// Bound by the latency of offsets, then rows and weights, then the join, around one burst: one token x 8 of 64 experts,
+// 2048 x 1024, 9.5 + 6.6 us (33.8 and 17.2 MB); 5 rows x 2048 -> 2048 4.6 us (stream_fp8 8.5).
 constexpr int kFewBlocksHeld = 2;        // blocks of K in flight per wave
 constexpr int kSplit = kWavesS;
 

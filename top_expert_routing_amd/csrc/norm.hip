@@ -4,7 +4,8 @@
 // The norm of a row r multiplies all of it by one number, rstd, so codes do not depend on it: they are
 // those of p = r * w, and rstd only multiplies their scale.  So one pass over the row in registers yields
 // the sum of squares and every maximum, and one exchange between the wavefronts joins them.
-// Bound by memory: x, residual, residual, y and codes are 2 + 2 + 2 + 2 + 1 bytes a value in bf16.
+// Bound by memory: x, residual, residual, y and codes are 2 + 2 + 2 + 2 + 1 bytes a value in bf16.  8191 x 2880 so:
+// 44.5 us (4.8 TB/s; a copy runs at 4.9); 4159 x 2048 with an fp32 residual and int8 codes alone 16.5 us.
 // A block of four wavefronts takes a row, or, where a row has no more values than the loads of one
 // wavefront, each wavefront one.  Rows of more than 256 * 8 * kMaxHeld values are read twice.
 #include "fp8_block.h"
@@ -179,6 +180,7 @@ void launch_norm_rows(const NormArgs& a, hipStream_t stream) {
 
 // ---- quantiser ------------------------------------------------------------------------
 // 16 lanes take the 128 columns of a block, eight values each; n blocks from block `first`, nb in a row.
+// 8191 x 2880 fp32: 17 us, 7 TB/s, so part of the rows comes from the last-level cache.
 constexpr int kBlocksPer = kThreads / 16;
 
 template <bool BF16>
