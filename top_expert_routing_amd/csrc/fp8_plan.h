@@ -35,6 +35,9 @@ using TileExact = TileCfg<4, 4, 2, 2, 4>;   // 128 rows x 128
 
 constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile: a row list arrives within them (tile_fp8)
 constexpr int kScaleGroup = 4;           // stages whose scales are loaded together
+// A tile is written down when the one before it begins to be requested, and stages are requested at most STAGES steps before
+// they are multiplied: by the time that a tile is stored, three later ones are written down with the shortest tiles.
+constexpr int kItemSlots = 8;
 template <class C, Mode M>
 struct TileLds {
   static constexpr int A = C::BM * kBlock, B = C::BN * kHalf;  // bytes of a stage's rows, of half a stage's weights
@@ -48,7 +51,8 @@ struct TileLds {
   static constexpr int LIST = SCALE0 + GROUPS * SCALES;        // row lists of two tiles
   static constexpr int MAX = LIST + 2 * C::BM * 4;             // kGateUp: largest magnitudes
   static constexpr int ZERO = MAX + (M == kGateUp ? C::WN * C::BM * 4 : 0);
-  static constexpr int PLAN = ZERO + 16;                       // sums over waves, tiles before each group, group offsets
+  static constexpr int ITEMS = ZERO + 16;                      // the tiles that are loaded and multiplied
+  static constexpr int PLAN = ITEMS + kItemSlots * static_cast<int>(sizeof(Item));                        // sums over waves, tiles before each group, group offsets
   static constexpr int bytes(int G) { return PLAN + 4 * (C::NW + kLoaders) + 8 * (G + 1); }
 };
 constexpr int kTileMostGroups = 800;     // whose lists fit beside the stages
