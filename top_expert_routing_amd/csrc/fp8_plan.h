@@ -69,15 +69,16 @@ inline Launch launch_of(const Plan& p) { return i8::launch_of(i8::Plan{i8::Kerne
 
 // Where tile_fp8 takes over from stream_fp8: few rows per group leave its tiles of 128 empty, and a small output
 // leaves CUs without one, each of them as long as K.  us, stream_fp8 / tile_fp8 (products alone of 2^20 outputs, FFNs of groups):
-//   outputs  linear 2048 -> 2048, 1024 rows (2.0) 20.9 / 22.5, 1536 rows (3.0) 28.8 / 23.4; 1024 -> 512, 2048 rows (1.0)
-//            13.5 / 15.5, 3000 rows (1.5) 18.7 / 15.8; 2560 -> 2560, 512 rows (1.3) 22.3 / 25.5, 768 rows (1.9) 31.2 / 26.2;
-//            fp32 out: 2048 -> 2048, 1536 rows 28.7 / 25.6; 1024 -> 512, 2048 rows 13.5 / 16.0
+//   outputs  linear 2048 -> 2048, 1024 rows (2.0) 21.1 / 22.0, 1536 rows (3.0) 28.9 / 22.7; 1024 -> 512, 2048 rows (1.0)
+//            13.8 / 14.9, 3000 rows (1.5) 19.1 / 15.1; 2560 -> 2560, 512 rows (1.3) 23.2 / 24.7, 768 rows (1.9) 31.4 / 25.1;
+//            fp32 out: 2048 -> 2048, 1536 rows 28.6 / 25.8; 1024 -> 512, 2048 rows 14.4 / 16.0
 //   rows     where every group's one tile makes kTileManyItems (three a CU), fewer rows are enough: groups' sizes even / falling
-//            as 1 / rank: FFN of 128 groups, 2880 x 2880, 24 rows 577 / 631 and 502 / 458, 28 rows 596 / 618 and 531 / 472, 34
-//            rows 684 / 631 and 598 / 508; 128 groups, 2048 x 768, 20 rows 142 / 140 and 123 / 126, 28 rows 144 / 143 and 140 /
-//            130; else: 64 groups, 2048 x 1024, 39 rows 107 / 105 and 105 / 125, 64 rows 125 / 108 and 126 / 128
-//            fp32 out: 64 groups 2048 -> 1024, 32 rows 36.5 / 44.1, 64 rows 46.0 / 46.6
-constexpr int kTileMinAvg = 48, kTileMinAvgMany = 28, kTileMinAvgExact = 64, kTileManyItems = 768;
+//            as 1 / rank: FFN of 128 groups, 2880 x 2880, 20 rows 574 / 587 and 463 / 404, 28 rows 589 / 600 and 526 / 453, 34
+//            rows 672 / 603 and 579 / 481; 128 groups, 2048 x 768, 20 rows 145 / 137 and 122 / 119, 28 rows 145 / 138 and 140 /
+//            122; else: 64 groups, 2048 x 1024, 34 rows 103 / 104 and 102 / 116, 48 rows 107 / 104 and 118 / 117; 32 groups,
+//            2880 x 2880, 28 rows 180 / 180 and 189 / 188, 39 rows 210 / 181 and 213 / 204
+//            fp32 out: 64 groups 2048 -> 1024, 48 rows 40.3 / 43.1, 64 rows 46.5 / 45.1
+constexpr int kTileMinAvg = 40, kTileMinAvgMany = 20, kTileMinAvgExact = 64, kTileManyItems = 768;
 constexpr long long kTileMinOutputs = 7 << 18;
 
 // Rows of stream_fp8's tiles, 16 * mf: 16 only where that leaves no CU a second item.  us with 16 / 32 rows: linear
