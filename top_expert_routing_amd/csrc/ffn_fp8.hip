@@ -416,12 +416,13 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_fp8(ProductArg
 // stages load while this one finishes.
 // Some waves multiply and four load.  A wave that requests an LDS-DMA load waits while the CU's address unit is
 // busy, and it is busy most of the time: where all waves did both, a tile's time was the sum of the two (FFN of
-// 96 rows for each of 64 experts, 2048 x 1024, 123 us with tiles of this size, 109 with waves that load; of 256 rows 238 / 195;
+// 96 rows for each of 64 experts, 2048 x 1024, 123 us with tiles of this size, 109 with waves that load; of 256 rows 238 / 191;
 // 8192 rows x 8192 -> 4096 265 us with tiles of 256 x 256, 270 with these of 128 x 256).
 // What bounds it: at 8192 x 8192 -> 4096 the loads alone take 214 us (159 from a warm L2), the matrix instructions alone 134,
 // those with their LDS reads 234.
 // EXACT (fp32 out) multiplies codes widened to bf16, at half the rate and with 16 conversions for each operand: four waves of
-// 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 166 us instead of 174).
+// 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 161 us;
+// 174 and 166 before the next tile was found early).
 //   * rows: 128 bytes of a row per stage, eight 16-byte pieces; piece c of row r lies at slot
 //     c ^ ((r / 2) % 8), so that the 16 rows of an operand read hit different banks.  A DMA instruction
 //     fills 8 rows (lane -> row lane / 8, slot lane % 8).
