@@ -201,3 +201,14 @@ def test_layer_refusals():
     layer.fp8_block_weights = q[:5] + (q[5][:, :1],)
     with pytest.raises(ValueError):
         layer.bound_calls(wl.logits, wl.x)
+
+
+def test_router_weights_are_of_the_rows_that_it_reads():
+    """The norm's rows are bf16, so an fp32 router matrix does not go with them, nor one of another width."""
+    wl, w, wr, _ = _case(5, 0, 0)
+    q = _blocks(wl.w_gate, wl.w_up, wl.w_down)
+    for bad in (wr.float(), wr[:, :64].contiguous(), wr[:8]):
+        layer = _layer(wl, 0, 0, fp8_block_weights=q, norm=(w, EPS), w_router=bad)
+        for call in (layer.forward, layer.bound_calls):
+            with pytest.raises((TypeError, ValueError)):
+                call(wl.logits, wl.x)

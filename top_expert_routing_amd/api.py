@@ -1202,6 +1202,7 @@ class MoeLayer:
             x = x if self.xn is None else self.xn
             dt = _dtype_code(self.h_sorted)
         if self.w_router is not None:
+            _out(self.w_router, "w_router", x.dtype, (E, self.d))
             logits = self.logits
             calls.append(("moe_router", lib.moe_router, (x.data_ptr(), self.w_router.data_ptr(), T, self.d, E, dt,
                                                          logits.data_ptr(), st)))

@@ -421,8 +421,8 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_fp8(ProductArg
 // What bounds it: at 8192 x 8192 -> 4096 the loads alone take 214 us (159 from a warm L2), the matrix instructions alone 134,
 // those with their LDS reads 234.
 // EXACT (fp32 out) multiplies codes widened to bf16, at half the rate and with 16 conversions for each operand: four waves of
-// 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 161 us;
-// 174 and 166 before the next tile was found early).
+// 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 166 us against 174, and 161 since the next
+// tile is found early).
 //   * rows: 128 bytes of a row per stage, eight 16-byte pieces; piece c of row r lies at slot
 //     c ^ ((r / 2) % 8), so that the 16 rows of an operand read hit different banks.  A DMA instruction
 //     fills 8 rows (lane -> row lane / 8, slot lane % 8).
