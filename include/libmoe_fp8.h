@@ -85,13 +85,12 @@ moe_status moe_grouped_linear_fp8(const void* xq, const float* x_scale, const in
 /*
  * moe_grouped_ffn_fp8 - the grouped SwiGLU expert FFN on block-scaled E4M3 rows
  * and weights (moe_rmsnorm or moe_quantize_blocks_fp8 make the rows), bf16 out:
- *     g = x . W_gate,  u = x . W_up   as in moe_grouped_linear_fp8 with a bf16
- *                                     result, but kept in fp32
+ *     g = x . W_gate,  u = x . W_up   as in moe_grouped_linear_fp8 with an fp32 result
  *     a = silu(g) * u in fp32, as codes and a scale for each 128 columns
- *     h = a . W_down                  likewise, rounded once to bf16.
- * g, u, silu, the scales and the quotients are fp32 steps (the hardware's
- * exponential and reciprocal among them), so a code whose quotient lies next to a
- * border between two codes may be the neighbour.  A block of the SwiGLU product
+ *     h = a . W_down                  as in moe_grouped_linear_fp8 with a bf16 result.
+ * g, u, silu, the scales and the quotients are fp32 steps whatever the batch (the
+ * hardware's exponential and reciprocal among them), so a code whose quotient lies
+ * next to a border between two codes may be the neighbour.  A block of the SwiGLU product
  * whose scale is below 2^-100 counts as zeros.
  *
  *   xq, x_scale    as in moe_grouped_linear_fp8 with K = d.

@@ -11,9 +11,10 @@
 //
 // The FP8 matrix instructions do not add in fp32: of each 8 columns of K they cut every product to a multiple of
 // 2^(e - 13), e the exponent of the largest of the eight (measured: 1.5e-5 to 5e-5 of a sum in the 2-norm).
-// tile_fp8 uses them where the result is rounded to bf16 (2^-9 of a value and more), at twice the rate.  Where it is
-// fp32, and in the kernels of fewer rows, which wait for memory, the codes are widened to bf16, which has every
-// E4M3 value, and multiplied by v_mfma_f32_16x16x32_bf16.
+// tile_fp8 uses them where the result itself is rounded to bf16 (2^-9 of a value and more), at twice the rate.  Where it
+// stays fp32, as for the gate and up sums, whose SwiGLU product is coded (cut sums turn one code of 650 into another one),
+// and in the kernels of fewer rows, which wait for memory, the codes are widened to bf16, which has every E4M3 value,
+// and multiplied by v_mfma_f32_16x16x32_bf16.
 //
 // Which of the 128 columns a lane holds does not matter as long as both operands agree:
 // lane 16 q + r holds columns 16 q .. 16 q + 15 and 64 + 16 q .. 64 + 16 q + 15 of row r, which
@@ -87,8 +88,8 @@ __device__ __forceinline__ f32x4 mfma_codes(const uint4 (&w)[2], const uint4 (&x
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Codes of the SwiGLU product from v * (1 / scale) without the exact quotient's correction: the
-// products carry larger errors (silu_mul), so a code may be the neighbour next to a border anyhow.
+// Codes of the SwiGLU product from v * (1 / scale) without the exact quotient's correction: v carries
+// larger errors (fp32 sums, silu_mul), so a code may be the neighbour next to a border anyhow (measured: one of 2e5).
 __device__ __forceinline__ Fp8Scale block_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7f800000u) return Fp8Scale{__builtin_nanf(""), 0.f};
   const float s = __uint_as_float(amax_bits) * (1.0f / 448.0f);
@@ -418,11 +419,15 @@ __global__ __launch_bounds__(kThreadsS, NC == 1 ? 4 : 2) void few_fp8(ProductArg
 // busy, and it is busy most of the time: where all waves did both, a tile's time was the sum of the two (FFN of
 // 96 rows for each of 64 experts, 2048 x 1024, 123 us with tiles of this size, 109 with waves that load; of 256 rows 238 / 191;
 // 8192 rows x 8192 -> 4096 265 us with tiles of 256 x 256, 270 with these of 128 x 256).
+// (FFN figures here and below compare two forms with both products on the FP8 instructions and 128 x 256 tiles.)
 // What bounds it: at 8192 x 8192 -> 4096 the loads alone take 214 us (159 from a warm L2), the matrix instructions alone 134,
 // those with their LDS reads 234.
-// EXACT (fp32 out) multiplies codes widened to bf16, at half the rate and with 16 conversions for each operand: four waves of
-// 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 166 us against 174, and 161 since the next
-// tile is found early).
+// EXACT (fp32 out, and kGateUp) multiplies codes widened to bf16, at half the rate and with 16 conversions for each operand: four
+// waves of 64 x 64, which share more of them than eight of 32 x 64 (8191 rows x 2048 -> 4096 166 us against 174, and 161 since
+// the next tile is found early).  kGateUp's tile is 64 x 256, since it holds the columns of one scale twice, of gate and of up:
+// FFN of 4096 tokens x 8 of 128 experts, 2048 x 768, 398 us, with eight waves of 32 x 64 405, on 128 x 256 with eight of 64 x 64,
+// whose registers leave the widened operands no room to stay, 407; of 34 rows for each of 128 experts, 2880 x 2880, 613, 617, 850.
+// (On the FP8 instructions, with cut sums, 298 and 618.)
 //   * rows: 128 bytes of a row per stage, eight 16-byte pieces; piece c of row r lies at slot
 //     c ^ ((r / 2) % 8), so that the 16 rows of an operand read hit different banks.  A DMA instruction
 //     fills 8 rows (lane -> row lane / 8, slot lane % 8).
@@ -866,6 +871,8 @@ void launch_many(const ProductArgs& p, hipStream_t stream) {
     else hipLaunchKernelGGL((stream_fp8<2, M, Out>), grid, block, 0, stream, p);
   } else if constexpr (exact) {
     launch_tile<TileExact, M, true, Out>(p, stream);
+  } else if constexpr (M == kGateUp) {                       // its sums stay fp32 until they are coded
+    launch_tile<TileGateUp, M, true, Out>(p, stream);
   } else {
     launch_tile<TileCodes, M, false, Out>(p, stream);
   }

@@ -32,6 +32,7 @@ struct TileCfg {
 };
 using TileCodes = TileCfg<4, 4, 2, 4, 3>;   // 128 rows x 256 weight rows
 using TileExact = TileCfg<4, 4, 2, 2, 4>;   // 128 rows x 128
+using TileGateUp = TileCfg<4, 4, 1, 4, 3>;  // 64 rows x 128 gate and the same 128 up rows
 
 constexpr int kTileMinStages = 3;        // fewest stages (blocks of K) of a tile: a row list arrives within them (tile_fp8)
 constexpr int kScaleGroup = 4;           // stages whose scales are loaded together
@@ -56,10 +57,12 @@ struct TileLds {
   static constexpr int bytes(int G) { return PLAN + 4 * (C::NW + kLoaders) + 8 * (G + 1); }
 };
 constexpr int kTileMostGroups = 800;     // whose lists fit beside the stages
-static_assert(TileLds<TileCodes, kGateUp>::bytes(kTileMostGroups) <= i8::kLdsPerCu &&
+static_assert(TileLds<TileCodes, kLinear>::bytes(kTileMostGroups) <= i8::kLdsPerCu &&
+              TileLds<TileGateUp, kGateUp>::bytes(kTileMostGroups) <= i8::kLdsPerCu &&
               TileLds<TileExact, kLinear>::bytes(kTileMostGroups) <= i8::kLdsPerCu, "a block's LDS");
 
-enum class Kernel { kFew, kStream, kTileCodes, kTileExact };
+// kTile: results of 16 bits or fewer (TileCodes; kGateUp: TileGateUp), kTileExact: fp32 results
+enum class Kernel { kFew, kStream, kTile, kTileExact };
 struct Plan {
   Kernel kernel;
   int width;    // few_fp8: 16-column blocks of an item; stream_fp8: 16-row blocks of a tile
@@ -73,10 +76,10 @@ inline Launch launch_of(const Plan& p) { return i8::launch_of(i8::Plan{i8::Kerne
 //            13.8 / 14.9, 3000 rows (1.5) 19.1 / 15.1; 2560 -> 2560, 512 rows (1.3) 23.2 / 24.7, 768 rows (1.9) 31.4 / 25.1;
 //            fp32 out: 2048 -> 2048, 1536 rows 28.6 / 25.8; 1024 -> 512, 2048 rows 14.4 / 16.0
 //   rows     where every group's one tile makes kTileManyItems (three a CU), fewer rows are enough: groups' sizes even / falling
-//            as 1 / rank: FFN of 128 groups, 2880 x 2880, 20 rows 574 / 587 and 463 / 404, 28 rows 589 / 600 and 526 / 453, 34
-//            rows 672 / 603 and 579 / 481; 128 groups, 2048 x 768, 20 rows 145 / 137 and 122 / 119, 28 rows 145 / 138 and 140 /
-//            122; else: 64 groups, 2048 x 1024, 34 rows 103 / 104 and 102 / 116, 48 rows 107 / 104 and 118 / 117; 32 groups,
-//            2880 x 2880, 28 rows 180 / 180 and 189 / 188, 39 rows 210 / 181 and 213 / 204
+//            as 1 / rank: FFN of 128 groups, 2880 x 2880, 16 rows 560 / 589 and 400 / 376, 20 rows 564 / 593 and 450 / 414, 28 rows
+//            597 / 600 and 536 / 481, 34 rows 692 / 606 and 600 / 527; 128 groups, 2048 x 768, 20 rows 143 / 139 and 124 / 119, 28
+//            rows 148 / 142 and 147 / 136; else: 64 groups, 2048 x 1024, 34 rows 105 / 104 and 104 / 115, 48 rows 111 / 108 and
+//            118 / 117; 32 groups, 2880 x 2880, 28 rows 179 / 177 and 190 / 193, 39 rows 215 / 184 and 218 / 206
 //            fp32 out: 64 groups 2048 -> 1024, 48 rows 40.3 / 43.1, 64 rows 46.5 / 45.1
 constexpr int kTileMinAvg = 40, kTileMinAvgMany = 20, kTileMinAvgExact = 64, kTileManyItems = 768;
 constexpr long long kTileMinOutputs = 7 << 18;
@@ -104,7 +107,7 @@ inline Plan many_plan(Mode m, bool exact, const Sizes& s) {
   const bool many = static_cast<long long>(s.sequences()) * ((s.cols + tile_cols - 1) / tile_cols) >= kTileManyItems;
   const int least = exact ? kTileMinAvgExact : many ? kTileMinAvgMany : kTileMinAvg;
   if (avg >= least && area >= kTileMinOutputs && s.K > (kTileMinStages - 1) * kBlock && s.groups() <= kTileMostGroups)
-    return Plan{exact ? Kernel::kTileExact : Kernel::kTileCodes, 0, 0};
+    return Plan{exact ? Kernel::kTileExact : Kernel::kTile, 0, 0};
   const int nch = (s.cols + kBlock - 1) / kBlock, mf = static_cast<long long>(max_m_tiles(s, 16)) * nch <= kSmallItems ? 1 : 2;
   return Plan{Kernel::kStream, mf, item_grid(max_m_tiles(s, 16 * mf), nch)};
 }
