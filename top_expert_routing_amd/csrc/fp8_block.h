@@ -12,14 +12,16 @@ constexpr int kFp8Block = 128;
 
 struct Fp8Scale {
   float base;    // divisor of the codes, and what is stored (times what the caller has left out of v)
-  float r;       // 1 / base, correctly rounded; 0 for values that are not all finite
+  float r;       // 1 / (base * up), correctly rounded; 0 for values that are not all finite
+  float up = 1.f;   // 2^64 for scales near the smallest (fp8_quotient)
 };
 
 __device__ __forceinline__ Fp8Scale fp8_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7f800000u) return Fp8Scale{__builtin_nanf(""), 0.f};
   const float s = __uint_as_float(amax_bits) * (1.0f / 448.0f);
   if (s < 0x1p-100f) return Fp8Scale{1.f, 1.f};
-  return Fp8Scale{s, 1.0f / s};
+  const float up = s < 0x1p-90f ? 0x1p64f : 1.f;
+  return Fp8Scale{s, 1.0f / (s * up), up};
 }
 
 // Four codes in a word, of quotients already taken.
@@ -30,11 +32,13 @@ __device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float 
 }
 
 // fl(v / base) from the correctly rounded reciprocal: v * r is within an ulp of the quotient, and
-// one step with the exact remainder rounds it correctly (Markstein).  base >= 2^-100 keeps the remainder
-// of every quotient that is not a zero code away from the subnormals.
+// one step with the exact remainder rounds it correctly (Markstein).  The remainder is a multiple of 2^(e - 46), e the
+// sum of the exponents of q and base, and exact while that is at least 2^-149.  Quotients that are not a zero code are
+// 2^-10 or more, so bases from 2^-90 on keep it exact; smaller ones are multiplied by 2^64 with their values, which
+// changes no quotient.
 __device__ __forceinline__ float fp8_quotient(float v, const Fp8Scale& s) {
-  const float q = v * s.r;
-  return __builtin_fmaf(__builtin_fmaf(-q, s.base, v), s.r, q);
+  const float x = v * s.up, q = x * s.r;
+  return __builtin_fmaf(__builtin_fmaf(-q, s.base * s.up, x), s.r, q);
 }
 
 __device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], const Fp8Scale& s) {
