@@ -789,7 +789,8 @@ def quantize_blocks_fp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Op
 
 def quantize_fp8_blocks(w: torch.Tensor):
     """E4M3 quantisation of [..][R][K] weights with a scale for each 128 x 128 block (the last ones may be
-    smaller): scale = max|block| * fl(1/448) (1 where that is below 2^-100), codes = w / scale to the nearest.
+    smaller): scale = max|block| * fl(1/448) (1 where that is below 2^-100), codes = w / scale to the nearest; scale NaN
+    and codes 0 for a block that is not all finite.
     Input preparation for the FP8 products, like quantize_fp8_rows; returns (codes float8_e4m3fn [..][R][K],
     scales fp32 [..][ceil(R / 128)][ceil(K / 128)])."""
     *lead, R, K = w.shape
@@ -798,8 +799,10 @@ def quantize_fp8_blocks(w: torch.Tensor):
     p = torch.nn.functional.pad(wf, (0, kb * FP8_BLOCK - K, 0, rb * FP8_BLOCK - R))
     s = p.reshape(*lead, rb, FP8_BLOCK, kb, FP8_BLOCK).abs().amax(dim=(-3, -1)) * (1.0 / 448.0)
     s = torch.where(s < 2.0 ** -100, torch.ones_like(s), s)
+    s = s.masked_fill(~torch.isfinite(s), float("nan"))
     wide = s.repeat_interleave(FP8_BLOCK, -2).repeat_interleave(FP8_BLOCK, -1)[..., :R, :K]
-    return (wf / wide).to(torch.float8_e4m3fn).contiguous(), s.contiguous()
+    codes = (wf / wide).masked_fill_(torch.isnan(wide), 0.0)
+    return codes.to(torch.float8_e4m3fn).contiguous(), s.contiguous()
 
 
 def _need_fp8_rows(xq: torch.Tensor, x_scale: torch.Tensor, index: int) -> None:
