@@ -329,6 +329,14 @@ def signature_recording(s, stats_ids, req_offsets, stream, K, dev, logits_stack=
             "pages_mi300x_per_request_us": {"scatter": 480.0, "d2h_staging": 210.0}}
 
 
+def ffn_call_bytes(used_experts, expert_bytes, N, d, esize, block):
+    """What one FFN call reads and writes at least: the used experts' weights, a row in and out per sorted row.
+    block: the rows in are E4M3 codes with an fp32 scale per 128 columns (the norm or the quantiser before the
+    call reads the tokens)."""
+    row_in = d + 4 * -(-d // 128) if block else d * esize
+    return used_experts * expert_bytes + N * row_in + N * d * esize
+
+
 def main():
     args = parse()
     if args.write_traffic:
@@ -529,7 +537,7 @@ def main():
     union = int(layer.stats_out["union_size"][0].item()) if layer.stats_out else s.E
     used_experts = union + s.S
     N = s.N
-    ffn_bytes = used_experts * expert_bytes + 2 * N * s.d * esize
+    ffn_bytes = ffn_call_bytes(used_experts, expert_bytes, N, s.d, esize, block)
     ffn_flops = 2.0 * N * 3 * s.d * s.I
     ffn_name = "moe_grouped_ffn_fp8" if block else "moe_grouped_ffn_i8" if int8 else \
         ("moe_grouped_ffn_fp8w_packed" if fp8_packed else "moe_grouped_ffn_fp8w") if fp8 else \
