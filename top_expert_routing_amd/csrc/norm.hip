@@ -5,9 +5,12 @@
 // those of p = r * w, and rstd only multiplies their scale.  So one pass over the row in registers yields
 // the sum of squares and every maximum, and one exchange between the wavefronts joins them.
 // Bound by memory: x, residual, residual, y and codes are 2 + 2 + 2 + 2 + 1 bytes a value in bf16.  8191 x 2880 so:
-// 44.5 us (4.8 TB/s; a copy runs at 4.9); 4159 x 2048 with an fp32 residual and int8 codes alone 16.5 us.
-// A block of four wavefronts takes a row, or, where a row has no more values than the loads of one
-// wavefront, each wavefront one.  Rows of more than 256 * 8 * kMaxHeld values are read twice.
+// 43.5 us (4.9 TB/s, as a copy runs); 4159 x 2048 with an fp32 residual and int8 codes alone 16.5 us.
+// A row has as few wavefronts as hold it with one piece a lane, one, two or four of them, and from 257 pieces on four with as
+// many pieces a lane as hold it (2, 4 or kMaxHeld); longer ones are read twice.  us of 23.6 million values, bf16 with a residual, y
+// and E4M3 codes, and of 16 rows: 512 columns one wavefront 41.3 / 3.2, two 46.4 / 3.4; 1024 two 41.2 / 3.4, four 46.1 /
+// 3.3; 2048 four with a piece each 40.3 / 3.3, with two 40.8 / 3.6; 2880 four with two 44.4 / 4.0, two with three 47.2 / 4.7, four
+// with four 47.4 / 4.5; 6144 four with four 46.5 / 5.0, with eight 51.6 / 5.9; 16384 with eight 49.7 / 8.4, read twice 55.0 / 10.0.
 #include "fp8_block.h"
 #include "launch.h"
 #include "row_piece.h"
@@ -171,7 +174,6 @@ void launch_norm_rows(const NormArgs& a, hipStream_t stream) {
   if (pieces <= 64) hipLaunchKernelGGL((rmsnorm<X, R, 64, 1>), grid(64), block, 0, stream, a);
   else if (pieces <= 128) hipLaunchKernelGGL((rmsnorm<X, R, 128, 1>), grid(128), block, 0, stream, a);
   else if (pieces <= 256) hipLaunchKernelGGL((rmsnorm<X, R, 256, 1>), grid(256), block, 0, stream, a);
-  else if (pieces <= 384) hipLaunchKernelGGL((rmsnorm<X, R, 128, 3>), grid(128), block, 0, stream, a);
   else if (pieces <= 512) hipLaunchKernelGGL((rmsnorm<X, R, 256, 2>), grid(256), block, 0, stream, a);
   else if (pieces <= 1024) hipLaunchKernelGGL((rmsnorm<X, R, 256, 4>), grid(256), block, 0, stream, a);
   else if (pieces <= 2048) hipLaunchKernelGGL((rmsnorm<X, R, 256, kMaxHeld>), grid(256), block, 0, stream, a);
