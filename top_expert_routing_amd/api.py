@@ -68,6 +68,12 @@ def _new(rows: int, cols: int, dtype, index: int) -> torch.Tensor:
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=index)
 
 
+def _int32_rows(x: torch.Tensor, d: int) -> None:
+    """The C calls take rows and columns as int32, and ctypes would pass on the low 32 bits of more."""
+    if d > 2 ** 31 - 1 or x.numel() > (2 ** 31 - 1) * d:
+        raise ValueError("x must have fewer than 2^31 rows and columns")
+
+
 def _call(name: str, index: int, fn, *args) -> None:
     """fn(*args, stream) on GPU `index` and its current stream."""
     if torch._C._cuda_getDevice() == index:
@@ -547,6 +553,7 @@ def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optio
         raise ValueError("x must have at least one dim")
     index = x.get_device()
     *rows, d = shape = x.shape
+    _int32_rows(x, d)
     if q is None:
         q = _new(*rows, d, torch.int8, index) if len(rows) == 1 else torch.empty(shape, dtype=torch.int8, device=index)
     elif not _ok(q, index, torch.int8, shape):
@@ -709,6 +716,7 @@ def _rows_of(x: torch.Tensor):
     if index < 0 or not shape or not x.is_contiguous():
         _need(x, "x")
         raise ValueError("x must have at least one dim")
+    _int32_rows(x, shape[-1])
     return index, shape, shape[-1]
 
 
