@@ -35,6 +35,9 @@ def _gpu():
     ("tile_codes", 1024, dict(sizes=[300, 1, 257, 700, 0, 64, 65, 800], T=900)),
     ("tile_codes", 2112, dict(sizes=[129, 640, 0, 500], T=700)),
     ("tile_codes", 1984, dict(sizes=[300, 0, 200], T=300, prio_sizes=[20, 64, 130], shared=1)),
+    # the shortest K of the tiles, its last block a half, and one stage more than the ring holds
+    ("tile_codes", 320, dict(sizes=[5600, 129, 0, 63, 1, 65], T=800)),
+    ("tile_codes", 448, dict(sizes=[1, 64, 4200, 127, 0], T=700)),
 ])
 def test_codes_are_those_of_fp32_sums(kernel, d, b):
     announce(f"ffn fp8 codes {kernel} {d}")
