@@ -70,6 +70,8 @@ moe_status moe_quantize_blocks_fp8(const void* x, moe_dtype dtype, int32_t T, in
  *   w        [E+n_shared][O][K] E4M3, packed (above).
  *   w_scale  [E+n_shared][ceil(O / 128)][ceil(K / 128)] fp32.
  *   y        [n_rows][O] of `out_dtype` (bf16 or fp32), written.
+ *   More than 800 groups (512 experts with a priority segment) run on the kernel of
+ *   small groups however many rows they have: fp32 sums, at a lower rate.
  *   Requires n_rows <= 2^24, K and O positive multiples of 64, nseg in {1, 2},
  *   1 <= E <= 512, n_shared <= 256; tensors of codes and values 16-byte aligned,
  *   scales 4-byte.
