@@ -70,7 +70,7 @@ struct Plan {
 };
 inline Launch launch_of(const Plan& p) { return i8::launch_of(i8::Plan{i8::Kernel::kStream, p.width, p.blocks}); }
 
-// Where tile_fp8 takes over from stream_fp8: few rows per group leave its tiles of 128 empty, and a small output
+// Where tile_fp8 takes over from stream_fp8: few rows per group leave its tiles of 128 (gate/up: 64) empty, and a small output
 // leaves CUs without one, each of them as long as K.  us, stream_fp8 / tile_fp8 (products alone of 2^20 outputs, FFNs of groups):
 //   outputs  linear 2048 -> 2048, 1024 rows (2.0) 21.1 / 22.0, 1536 rows (3.0) 28.9 / 22.7; 1024 -> 512, 2048 rows (1.0)
 //            13.8 / 14.9, 3000 rows (1.5) 19.1 / 15.1; 2560 -> 2560, 512 rows (1.3) 23.2 / 24.7, 768 rows (1.9) 31.4 / 25.1;
